@@ -28,7 +28,7 @@ lib = ctypes.CDLL(LIBRARY)
 ATTN_OK = 0
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_NULL", 2: "ATTN_ERR_INVALID", 3: "ATTN_ERR_UNSUPPORTED",
           4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_TIMEOUT", 6: "ATTN_ERR_DEVICE_BOUNDS",
-          7: "ATTN_ERR_SCRATCH_LIMIT"}
+          7: "ATTN_ERR_SCRATCH_LIMIT", 8: "ATTN_ERR_NO_PAGES"}
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
@@ -56,6 +56,28 @@ lib.attn_decode_paged.restype = _i
 lib.attn_decode_paged.argtypes = [_p, _p, _p, _p, _p, _p, _i, _p] + [_i] * 7
 lib.attn_decode_noalloc.restype = _i
 lib.attn_decode_noalloc.argtypes = [_p, _p, _p, _p, _p, _i, _p] + [_i] * 5
+lib.attn_fwd_sinks.restype = _i
+lib.attn_fwd_sinks.argtypes = [_p] * 5 + [_i] * 6 + [_f, _i, _i, _i, _p, _p, _p]
+lib.attn_bwd_sinks.restype = _i
+lib.attn_bwd_sinks.argtypes = [_p] * 9 + [_i] * 6 + [_f, _i, _i, _i, _p, _p, _p]
+lib.attn_decode_sinks.restype = _i
+lib.attn_decode_sinks.argtypes = [_p] * 5 + [_i] * 3 + [_p] + [_i] * 5
+lib.attn_decode_paged_sinks.restype = _i
+lib.attn_decode_paged_sinks.argtypes = [_p] * 6 + [_i] * 3 + [_p] + [_i] * 7
+lib.attn_tree_paged.restype = _i
+lib.attn_tree_paged.argtypes = [_p] * 9 + [_i] * 8
+lib.attn_cache_append.restype = _i
+lib.attn_cache_append.argtypes = [_p] * 8 + [_i] * 7
+lib.attn_cache_compact.restype = _i
+lib.attn_cache_compact.argtypes = [_p] * 7 + [_i] * 7
+lib.attn_cache_copy_blocks.restype = _i
+lib.attn_cache_copy_blocks.argtypes = [_p] * 5 + [_i] * 5
+lib.attn_cache_fork.restype = _i
+lib.attn_cache_fork.argtypes = [_p] * 8 + [_i] * 5
+lib.attn_cache_extend.restype = _i
+lib.attn_cache_extend.argtypes = [_p] * 5 + [_i] * 4
+lib.attn_cache_free.restype = _i
+lib.attn_cache_free.argtypes = [_p] * 6 + [_i] * 4
 lib.attn_status_string.restype = ctypes.c_char_p
 lib.attn_status_string.argtypes = [_i]
 lib.attn_last_device_status.restype = _i
@@ -208,6 +230,14 @@ def attn_bwd(dQ, dK, dV, dO, Q, K, V, O, LSE, scale, causal=False, window=0, inp
              k_lengths=None, q_lengths=None, stream=None):
     """Backward of attn_fwd: fill dQ (like Q) and dK, dV (like K, V) in place from dO,
     the forward's inputs, output O and LSE."""
+    B, Hq, Hkv, Sq, Sk, D = _check_backward(dQ, dK, dV, dO, Q, K, V, O, LSE, k_lengths, q_lengths)
+    rc = lib.attn_bwd(_ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
+                      _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale), int(causal), int(window),
+                      int(input_pos), _ptr(k_lengths), _ptr(q_lengths), _stream(stream))
+    _check(rc, "attn_bwd")
+
+
+def _check_backward(dQ, dK, dV, dO, Q, K, V, O, LSE, k_lengths, q_lengths):
     B, Hq, Hkv, Sq, Sk, D = _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths)
     if LSE is None:
         raise ValueError("LSE (the forward's saved statistics) is required")
@@ -217,10 +247,7 @@ def attn_bwd(dQ, dK, dV, dO, Q, K, V, O, LSE, scale, causal=False, window=0, inp
     _tensor(dV, "dV", torch.bfloat16, (B, Hkv, Sk, D))
     _same_device(dQ=dQ, dK=dK, dV=dV, dO=dO, Q=Q, K=K, V=V, O=O, LSE=LSE, k_lengths=k_lengths,
                  q_lengths=q_lengths)
-    rc = lib.attn_bwd(_ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
-                      _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale), int(causal), int(window),
-                      int(input_pos), _ptr(k_lengths), _ptr(q_lengths), _stream(stream))
-    _check(rc, "attn_bwd")
+    return B, Hq, Hkv, Sq, Sk, D
 
 
 def block_mask_shape(Sq: int, Sk: int):
@@ -294,6 +321,182 @@ def attn_decode_noalloc(O, Q, K, V, lengths, n_splits=8, stream=None):
     rc = lib.attn_decode_noalloc(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(lengths),
                                  int(n_splits), _stream(stream), B, Hq, Hkv, S_cap, D)
     _check(rc, "attn_decode_noalloc")
+
+
+def attn_fwd_sinks(O, Q, K, V, LSE, scale, window, sinks, input_pos=0, k_lengths=None,
+                   q_lengths=None, stream=None):
+    """attn_fwd, causal, with a sliding window and the first ``sinks`` keys always visible:
+    query position p sees keys j <= p with j > p - window or j < sinks."""
+    B, Hq, Hkv, Sq, Sk, D = _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths)
+    _same_device(O=O, Q=Q, K=K, V=V, LSE=LSE, k_lengths=k_lengths, q_lengths=q_lengths)
+    rc = lib.attn_fwd_sinks(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D,
+                            float(scale), int(window), int(sinks), int(input_pos),
+                            _ptr(k_lengths), _ptr(q_lengths), _stream(stream))
+    _check(rc, "attn_fwd_sinks")
+
+
+def attn_bwd_sinks(dQ, dK, dV, dO, Q, K, V, O, LSE, scale, window, sinks, input_pos=0,
+                   k_lengths=None, q_lengths=None, stream=None):
+    """Backward of attn_fwd_sinks: fill dQ (like Q) and dK, dV (like K, V) in place."""
+    B, Hq, Hkv, Sq, Sk, D = _check_backward(dQ, dK, dV, dO, Q, K, V, O, LSE, k_lengths, q_lengths)
+    rc = lib.attn_bwd_sinks(_ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V),
+                            _ptr(O), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale), int(window),
+                            int(sinks), int(input_pos), _ptr(k_lengths), _ptr(q_lengths),
+                            _stream(stream))
+    _check(rc, "attn_bwd_sinks")
+
+
+def attn_decode_sinks(O, Q, K, V, lengths, window, sinks, n_splits=0, stream=None):
+    """attn_decode of the last cached token with a sliding window and sinks: it sees keys
+    j < lengths[b] with j >= lengths[b] - window or j < sinks.  n_splits 0: the library's
+    choice."""
+    B, Hq, Hkv, S_cap, D = _check_decode(O, Q, K, V, lengths)
+    rc = lib.attn_decode_sinks(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(lengths), int(window),
+                               int(sinks), int(n_splits), _stream(stream), B, Hq, Hkv, S_cap, D)
+    _check(rc, "attn_decode_sinks")
+
+
+def attn_decode_paged_sinks(O, Q, K_cache, V_cache, block_tables, seq_lens, window, sinks,
+                            n_splits=0, stream=None):
+    """attn_decode_sinks from a paged cache; table entries of pages without a visible key
+    are not read."""
+    B, Hq, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 3)
+    _tensor(O, "O", torch.bfloat16, (B, Hq, D))
+    num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
+    _tensor(seq_lens, "seq_lens", torch.int32, (B,))
+    _same_device(O=O, Q=Q, K_cache=K_cache, V_cache=V_cache, block_tables=block_tables,
+                 seq_lens=seq_lens)
+    rc = lib.attn_decode_paged_sinks(_ptr(O), _ptr(Q), _ptr(K_cache), _ptr(V_cache),
+                                     _ptr(block_tables), _ptr(seq_lens), int(window), int(sinks),
+                                     int(n_splits), _stream(stream), B, Hq, Hkv, num_blocks,
+                                     block_size, max_blocks, D)
+    _check(rc, "attn_decode_paged_sinks")
+
+
+def attn_tree_paged(O, Q, K_cache, V_cache, block_tables, context_lens, parents, draft_lens=None,
+                    stream=None):
+    """Attention of T drafted tokens per sequence: Q, O (B,Hq,T,D); draft i stands at cache
+    position context_lens[b] + i, continues draft parents[b][i] (-1: the context) and sees the
+    context, itself and its ancestors.  Rows past draft_lens[b] (int32 (B,), or None = T) get 0."""
+    B, Hq, T, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 4)
+    _tensor(O, "O", torch.bfloat16, (B, Hq, T, D))
+    num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
+    _tensor(context_lens, "context_lens", torch.int32, (B,))
+    _tensor(parents, "parents", torch.int32, (B, T))
+    if draft_lens is not None:
+        _tensor(draft_lens, "draft_lens", torch.int32, (B,))
+    _same_device(O=O, Q=Q, K_cache=K_cache, V_cache=V_cache, block_tables=block_tables,
+                 context_lens=context_lens, parents=parents, draft_lens=draft_lens)
+    rc = lib.attn_tree_paged(_ptr(O), _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(block_tables),
+                             _ptr(context_lens), _ptr(parents), _ptr(draft_lens), _stream(stream),
+                             B, Hq, Hkv, T, num_blocks, block_size, max_blocks, D)
+    _check(rc, "attn_tree_paged")
+
+
+def _check_pool(K_cache, V_cache, block_tables, B, D):
+    num_blocks, block_size, Hkv, _ = _tensor(K_cache, "K_cache", torch.bfloat16,
+                                             (None, None, None, D))
+    _tensor(V_cache, "V_cache", torch.bfloat16, (num_blocks, block_size, Hkv, D))
+    _, max_blocks = _tensor(block_tables, "block_tables", torch.int32, (B, None))
+    return num_blocks, block_size, Hkv, max_blocks
+
+
+def cache_append(K_cache, V_cache, K_new, V_new, block_tables, start, n_new=None, stream=None):
+    """Write K_new, V_new (B,Hkv,T,D) to positions start[b] + t of each sequence's pages, for
+    t < n_new[b] (int32 (B,), or None = T)."""
+    B, Hkv, T, D = _tensor(K_new, "K_new", torch.bfloat16, (None,) * 4)
+    _tensor(V_new, "V_new", torch.bfloat16, (B, Hkv, T, D))
+    num_blocks, block_size, heads, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
+    if heads != Hkv:
+        raise ValueError(f"K_cache has {heads} KV heads, K_new has {Hkv}")
+    _tensor(start, "start", torch.int32, (B,))
+    if n_new is not None:
+        _tensor(n_new, "n_new", torch.int32, (B,))
+    _same_device(K_cache=K_cache, V_cache=V_cache, K_new=K_new, V_new=V_new,
+                 block_tables=block_tables, start=start, n_new=n_new)
+    rc = lib.attn_cache_append(_ptr(K_cache), _ptr(V_cache), _ptr(K_new), _ptr(V_new),
+                               _ptr(block_tables), _ptr(start), _ptr(n_new), _stream(stream), B,
+                               Hkv, T, num_blocks, block_size, max_blocks, D)
+    _check(rc, "attn_cache_append")
+
+
+def cache_compact(K_cache, V_cache, block_tables, base, keep, n_keep=None, stream=None):
+    """In place: position base[b] + k of each sequence takes the row of position
+    base[b] + keep[b][k], for k < n_keep[b]; keep int32 (B,A) is increasing."""
+    B, A = _tensor(keep, "keep", torch.int32, (None, None))
+    D = K_cache.shape[-1] if isinstance(K_cache, torch.Tensor) and K_cache.dim() else None
+    num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
+    _tensor(base, "base", torch.int32, (B,))
+    if n_keep is not None:
+        _tensor(n_keep, "n_keep", torch.int32, (B,))
+    _same_device(K_cache=K_cache, V_cache=V_cache, block_tables=block_tables, base=base, keep=keep,
+                 n_keep=n_keep)
+    rc = lib.attn_cache_compact(_ptr(K_cache), _ptr(V_cache), _ptr(block_tables), _ptr(base),
+                                _ptr(keep), _ptr(n_keep), _stream(stream), B, Hkv, A, num_blocks,
+                                block_size, max_blocks, D)
+    _check(rc, "attn_cache_compact")
+
+
+def cache_copy_blocks(K_cache, V_cache, src, dst, stream=None):
+    """Page dst[i] takes the contents of page src[i] (int32 (N,), negative = no pair)."""
+    num_blocks, block_size, Hkv, D = _tensor(K_cache, "K_cache", torch.bfloat16, (None,) * 4)
+    _tensor(V_cache, "V_cache", torch.bfloat16, (num_blocks, block_size, Hkv, D))
+    (N,) = _tensor(src, "src", torch.int32, (None,))
+    _tensor(dst, "dst", torch.int32, (N,))
+    _same_device(K_cache=K_cache, V_cache=V_cache, src=src, dst=dst)
+    rc = lib.attn_cache_copy_blocks(_ptr(K_cache), _ptr(V_cache), _ptr(src), _ptr(dst),
+                                    _stream(stream), N, num_blocks, block_size, Hkv, D)
+    _check(rc, "attn_cache_copy_blocks")
+
+
+def _check_table(block_tables, ref_counts):
+    R, max_blocks = _tensor(block_tables, "block_tables", torch.int32, (None, None))
+    (num_blocks,) = _tensor(ref_counts, "ref_counts", torch.int32, (None,))
+    return R, max_blocks, num_blocks
+
+
+def cache_fork(block_tables, ref_counts, seq_lens, parents, children, copy_src, copy_dst,
+               block_size, stream=None):
+    """Table row children[n] continues row parents[n]: whole pages shared, a fresh page for the
+    part-filled one, whose copy is left to cache_copy_blocks(copy_src, copy_dst)."""
+    R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
+    _tensor(seq_lens, "seq_lens", torch.int32, (R,))
+    (N,) = _tensor(parents, "parents", torch.int32, (None,))
+    _tensor(children, "children", torch.int32, (N,))
+    _tensor(copy_src, "copy_src", torch.int32, (N,))
+    _tensor(copy_dst, "copy_dst", torch.int32, (N,))
+    _same_device(block_tables=block_tables, ref_counts=ref_counts, seq_lens=seq_lens,
+                 parents=parents, children=children, copy_src=copy_src, copy_dst=copy_dst)
+    rc = lib.attn_cache_fork(_ptr(block_tables), _ptr(ref_counts), _ptr(seq_lens), _ptr(parents),
+                             _ptr(children), _ptr(copy_src), _ptr(copy_dst), _stream(stream), N, R,
+                             num_blocks, int(block_size), max_blocks)
+    _check(rc, "attn_cache_fork")
+
+
+def cache_extend(block_tables, ref_counts, from_lens, to_lens, block_size, stream=None):
+    """Free pages for the empty entries of each row from the page of position from_lens[r] to
+    the last page that to_lens[r] tokens need."""
+    R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
+    _tensor(from_lens, "from_lens", torch.int32, (R,))
+    _tensor(to_lens, "to_lens", torch.int32, (R,))
+    _same_device(block_tables=block_tables, ref_counts=ref_counts, from_lens=from_lens,
+                 to_lens=to_lens)
+    rc = lib.attn_cache_extend(_ptr(block_tables), _ptr(ref_counts), _ptr(from_lens), _ptr(to_lens),
+                               _stream(stream), R, num_blocks, int(block_size), max_blocks)
+    _check(rc, "attn_cache_extend")
+
+
+def cache_free(block_tables, ref_counts, rows, first, last, stream=None):
+    """Give back table entries first[n] .. last[n]-1 of row rows[n] (int32 (N,))."""
+    R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
+    (N,) = _tensor(rows, "rows", torch.int32, (None,))
+    _tensor(first, "first", torch.int32, (N,))
+    _tensor(last, "last", torch.int32, (N,))
+    _same_device(block_tables=block_tables, ref_counts=ref_counts, rows=rows, first=first,
+                 last=last)
+    rc = lib.attn_cache_free(_ptr(block_tables), _ptr(ref_counts), _ptr(rows), _ptr(first),
+                             _ptr(last), _stream(stream), N, R, num_blocks, max_blocks)
+    _check(rc, "attn_cache_free")
 
 
 def last_device_status(stream=None) -> int:

@@ -2,6 +2,7 @@
 // host-side argument validation, TMA descriptor encoding, the per-device status
 // word, and the workspaces (from a per-device pool the library owns).
 #include <nvtx3/nvToolsExt.h>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -338,10 +339,44 @@ attn_status_t attn_fwd_flex(void *O, const void *Q, const void *K, const void *V
     return launch_fwd(a, static_cast<cudaStream_t>(stream));
 }
 
-attn_status_t attn_decode(void *O, const void *Q, const void *K, const void *V,
-                          const int32_t *lengths, int n_splits, void *stream, int B, int Hq,
-                          int Hkv, int S_cap, int D) {
-    NvtxRange nvtx_range("attn_decode");
+attn_status_t attn_fwd_sinks(void *O, const void *Q, const void *K, const void *V, float *LSE,
+                             int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale, int window,
+                             int sinks, int input_pos, const int32_t *k_lengths,
+                             const int32_t *q_lengths, void *stream) {
+    NvtxRange nvtx_range("attn_fwd_sinks");
+    attn_status_t st =
+        validate_fwd(O, Q, K, V, LSE, B, Hq, Hkv, Sq, Sk, D, scale, 1, window, input_pos);
+    if (st != ATTN_OK) return st;
+    if (window < 1 || sinks < 0) return ATTN_ERR_INVALID;
+    if ((long long)B * Hq * Sq == 0) return ATTN_OK;
+    FwdArgs a;
+    a.O = O;
+    a.Q = Q;
+    a.K = Sk > 0 ? K : Q;  // stand-in tensor map without a key
+    a.V = Sk > 0 ? V : Q;
+    a.LSE = LSE;
+    a.k_lengths = k_lengths;
+    a.q_lengths = q_lengths;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.Sq = Sq;
+    a.Sk = Sk;
+    a.D = D;
+    a.scale = scale;
+    a.causal = 1;
+    a.window = window;
+    a.sinks = sinks;
+    a.input_pos = input_pos;
+    return launch_fwd(a, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// attn_decode (window = 0) and attn_decode_sinks.
+attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const void *V,
+                                const int32_t *lengths, int window, int sinks, int n_splits,
+                                void *stream, int B, int Hq, int Hkv, int S_cap, int D) {
     if (B < 0 || Hq < 1 || Hkv < 1 || S_cap < 0 || n_splits < 1 || n_splits > 64)
         return ATTN_ERR_INVALID;
     if (Hq % Hkv != 0 || Hq / Hkv > 16) return ATTN_ERR_INVALID;
@@ -370,16 +405,51 @@ attn_status_t attn_decode(void *O, const void *Q, const void *K, const void *V,
     a.S_cap = S_cap;
     a.D = D;
     a.workspace = static_cast<float *>(ws);
+    a.window = window;
+    a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return st;
 }
 
-attn_status_t attn_bwd(void *dQ, void *dK, void *dV, const void *dO, const void *Q, const void *K,
+// Slices per (sequence, KV head) when the caller leaves them to the library: enough for
+// two blocks per SM, and at most one per 64-key tile that can hold a visible key.
+int sink_splits(int B, int Hkv, long long S_cap, int window, int sinks) {
+    const long long tiles = std::min((std::min<long long>(window, S_cap) + 62) / 64 + 1 +
+                                         (std::min<long long>(sinks, S_cap) + 63) / 64,
+                                     (S_cap + 63) / 64);
+    const long long pairs = std::max(1ll, (long long)B * Hkv);
+    return static_cast<int>(std::max(1ll, std::min({(2 * 148 + pairs - 1) / pairs, tiles, 64ll})));
+}
+
+}  // namespace
+
+attn_status_t attn_decode(void *O, const void *Q, const void *K, const void *V,
+                          const int32_t *lengths, int n_splits, void *stream, int B, int Hq,
+                          int Hkv, int S_cap, int D) {
+    NvtxRange nvtx_range("attn_decode");
+    return decode_contiguous(O, Q, K, V, lengths, 0, 0, n_splits, stream, B, Hq, Hkv, S_cap, D);
+}
+
+attn_status_t attn_decode_sinks(void *O, const void *Q, const void *K, const void *V,
+                                const int32_t *lengths, int window, int sinks, int n_splits,
+                                void *stream, int B, int Hq, int Hkv, int S_cap, int D) {
+    NvtxRange nvtx_range("attn_decode_sinks");
+    if (window < 1 || sinks < 0) return ATTN_ERR_INVALID;
+    if (n_splits == 0 && B >= 0 && Hkv >= 1 && S_cap >= 0)
+        n_splits = sink_splits(B, Hkv, S_cap, window, sinks);
+    return decode_contiguous(O, Q, K, V, lengths, window, sinks, n_splits, stream, B, Hq, Hkv, S_cap,
+                             D);
+}
+
+namespace {
+
+// attn_bwd (sinks = 0) and attn_bwd_sinks.
+attn_status_t backward(void *dQ, void *dK, void *dV, const void *dO, const void *Q, const void *K,
                        const void *V, const void *O, const float *LSE, int B, int Hq, int Hkv,
-                       int Sq, int Sk, int D, float scale, int causal, int window, int input_pos,
-                       const int32_t *k_lengths, const int32_t *q_lengths, void *stream) {
-    NvtxRange nvtx_range("attn_bwd");
+                       int Sq, int Sk, int D, float scale, int causal, int window, int sinks,
+                       int input_pos, const int32_t *k_lengths, const int32_t *q_lengths,
+                       void *stream) {
     attn_status_t st =
         validate_fwd(const_cast<void *>(O), Q, K, V, nullptr, B, Hq, Hkv, Sq, Sk, D, scale, causal,
                      window, input_pos);
@@ -424,10 +494,33 @@ attn_status_t attn_bwd(void *dQ, void *dK, void *dV, const void *dO, const void 
     a.causal = causal;
     a.window = window;
     a.input_pos = input_pos;
+    a.sinks = sinks;
     a.delta = static_cast<float *>(ws);
     st = launch_bwd(a, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return st;
+}
+
+}  // namespace
+
+attn_status_t attn_bwd(void *dQ, void *dK, void *dV, const void *dO, const void *Q, const void *K,
+                       const void *V, const void *O, const float *LSE, int B, int Hq, int Hkv,
+                       int Sq, int Sk, int D, float scale, int causal, int window, int input_pos,
+                       const int32_t *k_lengths, const int32_t *q_lengths, void *stream) {
+    NvtxRange nvtx_range("attn_bwd");
+    return backward(dQ, dK, dV, dO, Q, K, V, O, LSE, B, Hq, Hkv, Sq, Sk, D, scale, causal, window, 0,
+                    input_pos, k_lengths, q_lengths, stream);
+}
+
+attn_status_t attn_bwd_sinks(void *dQ, void *dK, void *dV, const void *dO, const void *Q,
+                             const void *K, const void *V, const void *O, const float *LSE, int B,
+                             int Hq, int Hkv, int Sq, int Sk, int D, float scale, int window,
+                             int sinks, int input_pos, const int32_t *k_lengths,
+                             const int32_t *q_lengths, void *stream) {
+    NvtxRange nvtx_range("attn_bwd_sinks");
+    if (window < 1 || sinks < 0) return ATTN_ERR_INVALID;
+    return backward(dQ, dK, dV, dO, Q, K, V, O, LSE, B, Hq, Hkv, Sq, Sk, D, scale, 1, window, sinks,
+                    input_pos, k_lengths, q_lengths, stream);
 }
 
 attn_status_t attn_rbs_block_mask(uint8_t *block_mask, float *base_scores, float *rescue_scores,
@@ -475,11 +568,13 @@ attn_status_t attn_rbs_block_mask(uint8_t *block_mask, float *base_scores, float
     return st;
 }
 
-attn_status_t attn_decode_paged(void *O, const void *Q, const void *K_cache, const void *V_cache,
-                                const int32_t *block_tables, const int32_t *seq_lens, int n_splits,
-                                void *stream, int B, int Hq, int Hkv, int num_blocks,
-                                int block_size, int max_blocks_per_seq, int D) {
-    NvtxRange nvtx_range("attn_decode_paged");
+namespace {
+
+// attn_decode_paged (window = 0) and attn_decode_paged_sinks.
+attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const void *V_cache,
+                           const int32_t *block_tables, const int32_t *seq_lens, int window,
+                           int sinks, int n_splits, void *stream, int B, int Hq, int Hkv,
+                           int num_blocks, int block_size, int max_blocks_per_seq, int D) {
     if (B < 0 || Hq < 1 || Hkv < 1 || num_blocks < 1 || max_blocks_per_seq < 0 || n_splits < 1 ||
         n_splits > 64)
         return ATTN_ERR_INVALID;
@@ -517,9 +612,248 @@ attn_status_t attn_decode_paged(void *O, const void *Q, const void *K_cache, con
     a.num_blocks = num_blocks;
     a.block_size = block_size;
     a.max_blocks = max_blocks_per_seq;
+    a.window = window;
+    a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return st;
+}
+
+// Sizes of a paged cache that every operator on it checks.
+attn_status_t validate_pool(int num_blocks, int block_size, int max_blocks) {
+    if (num_blocks < 1 || max_blocks < 1) return ATTN_ERR_INVALID;
+    if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1)) != 0)
+        return ATTN_ERR_INVALID;
+    if ((long long)num_blocks * block_size > 0x7fffffffll ||
+        (long long)max_blocks * block_size > 0x7fffffffll)
+        return ATTN_ERR_INVALID;
+    return ATTN_OK;
+}
+
+// int32 arrays of the cache operators: given, and 16-byte aligned where read in vectors.
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+attn_status_t attn_decode_paged(void *O, const void *Q, const void *K_cache, const void *V_cache,
+                                const int32_t *block_tables, const int32_t *seq_lens, int n_splits,
+                                void *stream, int B, int Hq, int Hkv, int num_blocks,
+                                int block_size, int max_blocks_per_seq, int D) {
+    NvtxRange nvtx_range("attn_decode_paged");
+    return decode_paged(O, Q, K_cache, V_cache, block_tables, seq_lens, 0, 0, n_splits, stream, B, Hq,
+                        Hkv, num_blocks, block_size, max_blocks_per_seq, D);
+}
+
+attn_status_t attn_decode_paged_sinks(void *O, const void *Q, const void *K_cache,
+                                      const void *V_cache, const int32_t *block_tables,
+                                      const int32_t *seq_lens, int window, int sinks, int n_splits,
+                                      void *stream, int B, int Hq, int Hkv, int num_blocks,
+                                      int block_size, int max_blocks_per_seq, int D) {
+    NvtxRange nvtx_range("attn_decode_paged_sinks");
+    if (window < 1 || sinks < 0) return ATTN_ERR_INVALID;
+    if (n_splits == 0 && B >= 0 && Hkv >= 1 && max_blocks_per_seq >= 0 && block_size > 0)
+        n_splits = sink_splits(B, Hkv, (long long)max_blocks_per_seq * block_size, window, sinks);
+    return decode_paged(O, Q, K_cache, V_cache, block_tables, seq_lens, window, sinks, n_splits, stream,
+                        B, Hq, Hkv, num_blocks, block_size, max_blocks_per_seq, D);
+}
+
+attn_status_t attn_tree_paged(void *O, const void *Q, const void *K_cache, const void *V_cache,
+                              const int32_t *block_tables, const int32_t *context_lens,
+                              const int32_t *parents, const int32_t *draft_lens, void *stream,
+                              int B, int Hq, int Hkv, int T, int num_blocks, int block_size,
+                              int max_blocks_per_seq, int D) {
+    NvtxRange nvtx_range("attn_tree_paged");
+    if (B < 0 || Hq < 1 || Hkv < 1 || T < 0 || T > 256) return ATTN_ERR_INVALID;
+    attn_status_t st = validate_pool(num_blocks, block_size, max_blocks_per_seq);
+    if (st != ATTN_OK) return st;
+    if (Hq % Hkv != 0 || Hq / Hkv > 16) return ATTN_ERR_INVALID;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)B * Hkv > 0x7fffffffll) return ATTN_ERR_INVALID;
+    if (B == 0 || T == 0) return ATTN_OK;
+    if (!O || !Q || !K_cache || !V_cache || !block_tables || !context_lens || !parents)
+        return ATTN_ERR_NULL;
+    if (!aligned16(O) || !aligned16(Q) || !aligned16(K_cache) || !aligned16(V_cache) ||
+        !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(parents) ||
+        !aligned4(draft_lens))
+        return ATTN_ERR_INVALID;
+    TreeArgs a;
+    a.O = O;
+    a.Q = Q;
+    a.K = K_cache;
+    a.V = V_cache;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.parents = parents;
+    a.draft_lens = draft_lens;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.T = T;
+    a.D = D;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    return launch_tree(a, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_cache_append(void *K_cache, void *V_cache, const void *K_new, const void *V_new,
+                                const int32_t *block_tables, const int32_t *start,
+                                const int32_t *n_new, void *stream, int B, int Hkv, int T,
+                                int num_blocks, int block_size, int max_blocks_per_seq, int D) {
+    NvtxRange nvtx_range("attn_cache_append");
+    if (B < 0 || Hkv < 1 || T < 0) return ATTN_ERR_INVALID;
+    attn_status_t st = validate_pool(num_blocks, block_size, max_blocks_per_seq);
+    if (st != ATTN_OK) return st;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0) return ATTN_OK;
+    if (!K_cache || !V_cache || !K_new || !V_new || !block_tables || !start) return ATTN_ERR_NULL;
+    if (!aligned16(K_cache) || !aligned16(V_cache) || !aligned16(K_new) || !aligned16(V_new) ||
+        !aligned4(block_tables) || !aligned4(start) || !aligned4(n_new))
+        return ATTN_ERR_INVALID;
+    CacheArgs a;
+    a.K = K_cache;
+    a.V = V_cache;
+    a.K_new = K_new;
+    a.V_new = V_new;
+    a.block_tables = block_tables;
+    a.start = start;
+    a.counts = n_new;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.T = T;
+    a.D = D;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    return launch_cache_append(a, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_cache_compact(void *K_cache, void *V_cache, const int32_t *block_tables,
+                                 const int32_t *base, const int32_t *keep, const int32_t *n_keep,
+                                 void *stream, int B, int Hkv, int A, int num_blocks,
+                                 int block_size, int max_blocks_per_seq, int D) {
+    NvtxRange nvtx_range("attn_cache_compact");
+    if (B < 0 || Hkv < 1 || Hkv > (1 << 24) || A < 0) return ATTN_ERR_INVALID;
+    attn_status_t st = validate_pool(num_blocks, block_size, max_blocks_per_seq);
+    if (st != ATTN_OK) return st;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (B == 0 || A == 0) return ATTN_OK;
+    if (!K_cache || !V_cache || !block_tables || !base || !keep) return ATTN_ERR_NULL;
+    if (!aligned16(K_cache) || !aligned16(V_cache) || !aligned4(block_tables) || !aligned4(base) ||
+        !aligned4(keep) || !aligned4(n_keep))
+        return ATTN_ERR_INVALID;
+    CacheArgs a;
+    a.K = K_cache;
+    a.V = V_cache;
+    a.block_tables = block_tables;
+    a.start = base;
+    a.keep = keep;
+    a.counts = n_keep;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.T = A;
+    a.D = D;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    return launch_cache_compact(a, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_cache_copy_blocks(void *K_cache, void *V_cache, const int32_t *src,
+                                     const int32_t *dst, void *stream, int N, int num_blocks,
+                                     int block_size, int Hkv, int D) {
+    NvtxRange nvtx_range("attn_cache_copy_blocks");
+    if (N < 0 || N > 65536 || Hkv < 1) return ATTN_ERR_INVALID;
+    attn_status_t st = validate_pool(num_blocks, block_size, 1);
+    if (st != ATTN_OK) return st;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (N == 0) return ATTN_OK;
+    if (!K_cache || !V_cache || !src || !dst) return ATTN_ERR_NULL;
+    if (!aligned16(K_cache) || !aligned16(V_cache) || !aligned4(src) || !aligned4(dst))
+        return ATTN_ERR_INVALID;
+    return launch_cache_copy(K_cache, V_cache, src, dst, N, num_blocks,
+                             (long long)block_size * Hkv * D * 2, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_t *seq_lens,
+                              const int32_t *parents, const int32_t *children, int32_t *copy_src,
+                              int32_t *copy_dst, void *stream, int N, int R, int num_blocks,
+                              int block_size, int max_blocks_per_seq) {
+    NvtxRange nvtx_range("attn_cache_fork");
+    if (N < 0 || N > 65536 || R < 0) return ATTN_ERR_INVALID;
+    attn_status_t st = validate_pool(num_blocks, block_size, max_blocks_per_seq);
+    if (st != ATTN_OK) return st;
+    if (N == 0) return ATTN_OK;
+    if (!block_tables || !ref_counts || !seq_lens || !parents || !children || !copy_src || !copy_dst)
+        return ATTN_ERR_NULL;
+    if (!aligned4(block_tables) || !aligned16(ref_counts) || !aligned4(seq_lens) ||
+        !aligned4(parents) || !aligned4(children) || !aligned4(copy_src) || !aligned4(copy_dst))
+        return ATTN_ERR_INVALID;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void *ws = nullptr;
+    if (workspace_alloc(&ws, (size_t)N * sizeof(int32_t), s) != cudaSuccess) return ATTN_ERR_CUDA;
+    CacheForkArgs a;
+    a.tables = block_tables;
+    a.refs = ref_counts;
+    a.lens = seq_lens;
+    a.parents = parents;
+    a.children = children;
+    a.copy_src = copy_src;
+    a.copy_dst = copy_dst;
+    a.N = N;
+    a.R = R;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.workspace = static_cast<int32_t *>(ws);
+    st = launch_cache_fork(a, s);
+    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    return st;
+}
+
+attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts, const int32_t *from_lens,
+                                const int32_t *to_lens, void *stream, int R, int num_blocks,
+                                int block_size, int max_blocks_per_seq) {
+    NvtxRange nvtx_range("attn_cache_extend");
+    if (R < 0) return ATTN_ERR_INVALID;
+    attn_status_t st = validate_pool(num_blocks, block_size, max_blocks_per_seq);
+    if (st != ATTN_OK) return st;
+    if (R == 0) return ATTN_OK;
+    if (!block_tables || !ref_counts || !from_lens || !to_lens) return ATTN_ERR_NULL;
+    if (!aligned4(block_tables) || !aligned16(ref_counts) || !aligned4(from_lens) ||
+        !aligned4(to_lens))
+        return ATTN_ERR_INVALID;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const long long ints = R + 1ll + std::min((long long)R * max_blocks_per_seq, (long long)num_blocks);
+    void *ws = nullptr;
+    if (workspace_alloc(&ws, (size_t)ints * sizeof(int32_t), s) != cudaSuccess) return ATTN_ERR_CUDA;
+    CacheExtendArgs a;
+    a.tables = block_tables;
+    a.refs = ref_counts;
+    a.from = from_lens;
+    a.to = to_lens;
+    a.R = R;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.max_blocks = max_blocks_per_seq;
+    a.workspace = static_cast<int32_t *>(ws);
+    st = launch_cache_extend(a, s);
+    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    return st;
+}
+
+attn_status_t attn_cache_free(int32_t *block_tables, int32_t *ref_counts, const int32_t *rows,
+                              const int32_t *first, const int32_t *last, void *stream, int N, int R,
+                              int num_blocks, int max_blocks_per_seq) {
+    NvtxRange nvtx_range("attn_cache_free");
+    if (N < 0 || R < 0 || num_blocks < 1 || max_blocks_per_seq < 1) return ATTN_ERR_INVALID;
+    if (N == 0) return ATTN_OK;
+    if (!block_tables || !ref_counts || !rows || !first || !last) return ATTN_ERR_NULL;
+    if (!aligned4(block_tables) || !aligned4(ref_counts) || !aligned4(rows) || !aligned4(first) ||
+        !aligned4(last))
+        return ATTN_ERR_INVALID;
+    return launch_cache_free(block_tables, ref_counts, rows, first, last, N, R, max_blocks_per_seq,
+                             num_blocks, static_cast<cudaStream_t>(stream));
 }
 
 const char *attn_status_string(attn_status_t status) {
@@ -534,6 +868,7 @@ const char *attn_status_string(attn_status_t status) {
         case ATTN_ERR_SCRATCH_LIMIT:
             return "ATTN_ERR_SCRATCH_LIMIT: workspace exceeds the 16 MiB fixed array of "
                    "attn_decode_noalloc";
+        case ATTN_ERR_NO_PAGES: return "ATTN_ERR_NO_PAGES: no free page left in the cache's pool";
     }
     return "unknown attn_status_t";
 }

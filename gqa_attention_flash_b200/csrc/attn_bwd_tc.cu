@@ -95,6 +95,7 @@ struct TcParams {
     int B, Hq, Hkv, Sq, Sk, group;
     float scale, scale_log2;
     int causal, window, input_pos;
+    int sinks;  // keys j < sinks stay visible outside the window (kSink only)
     uint64_t wait_limit_ns;
     int *status;
 };
@@ -132,17 +133,21 @@ __device__ __forceinline__ void tc_lengths(const TcParams &p, int b, int &k_end,
 // Visible pairs (query i, key j): i < q_end, j < k_end, causal j <= input_pos + i,
 // window j > input_pos + i - window.  For one key row j and the query tile at q0:
 // the visible tile columns are [lo, hi) (lo >= hi: none).
+// kSink: a key j < sinks has no window.
+template <bool kSink>
 __device__ __forceinline__ void cols_of_key(const TcParams &p, int j, int q0, int k_end, int q_end,
                                             int &lo, int &hi) {
     long long l = 0, h = min(TB, q_end - q0);
     if (p.causal) l = max(l, (long long)j - p.input_pos - q0);
-    if (p.window > 0) h = min(h, (long long)j + p.window - p.input_pos - q0);
+    if (p.window > 0 && !(kSink && j < p.sinks))
+        h = min(h, (long long)j + p.window - p.input_pos - q0);
     if (j >= k_end) h = 0;
     lo = static_cast<int>(max(0ll, min(l, (long long)TB)));
     hi = static_cast<int>(max(0ll, h));
 }
 
-// For one query row i and the key tile at kv0: visible tile columns [lo, hi).
+// For one query row i and the key tile at kv0: visible tile columns [lo, hi) (with
+// sinks: and those below both sinks - kv0 and hi).
 __device__ __forceinline__ void cols_of_query(const TcParams &p, int i, int kv0, int k_end, int q_end,
                                               int &lo, int &hi) {
     const long long pos = (long long)p.input_pos + i;
@@ -277,7 +282,7 @@ __device__ __forceinline__ void tc_zero_half(__nv_bfloat16 *dst, int c0) {
 // ---------------------------------------------------------------------------------
 // dK, dV of one 128-key tile
 // ---------------------------------------------------------------------------------
-template <int D>
+template <int D, bool kSink>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     int i_lo = 0, i_hi = q_end;
     if (kv0 >= k_end) i_hi = 0;
     if (p.causal) i_lo = max(0, kv0 - p.input_pos);
-    if (p.window > 0) i_hi = static_cast<int>(min((long long)i_hi, (long long)kv0 + TB + p.window - p.input_pos));
+    if (p.window > 0 && !(kSink && kv0 < p.sinks)) i_hi = static_cast<int>(min((long long)i_hi, (long long)kv0 + TB + p.window - p.input_pos));
     const int qt_lo = i_lo / TB, qt_hi = i_hi > i_lo ? (i_hi + TB - 1) / TB : qt_lo;
     const int n_qt = qt_hi - qt_lo, n_it = p.group * n_qt;
 
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const int q0 = (qt_lo + it % n_qt) * TB;
             const float *rows = reinterpret_cast<const float *>(smem + C::stage(st) + 2 * C::TILE);
             int lo, hi;
-            cols_of_key(p, j, q0, k_end, q_end, lo, hi);
+            cols_of_key<kSink>(p, j, q0, k_end, q_end, lo, hi);
             lo -= cb;
             hi -= cb;
             float pr[64];
@@ -576,7 +581,7 @@ struct DqCfg {
     static constexpr uint32_t COL_S = 0, COL_DP = 2 * TB, COL_DQ = 3 * TB;
 };
 
-template <int D>
+template <int D, bool kSink>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -600,7 +605,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int q0 = qt * TB;
     int k_end, q_end;
     tc_lengths(p, b, k_end, q_end);
-    int lo = 0, hi = 0;  // key tiles holding a key some row of this tile sees
+    // key tiles holding a key some row of this tile sees: [0, n_s) (sinks below the
+    // window) and [lo, hi); tile g of them is key_tile(g)
+    int lo = 0, hi = 0, n_s = 0;
     if (q0 < q_end && k_end > 0) {
         const int qlast = min(q0 + TB - 1, q_end - 1);
         long long h = k_end;
@@ -611,8 +618,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             lo = static_cast<int>(l / TB);
             hi = static_cast<int>((h + TB - 1) / TB);
         }
+        if constexpr (kSink) {
+            n_s = static_cast<int>((min(h, (long long)p.sinks) + TB - 1) / TB);
+            if (h > l) n_s = min(n_s, lo);
+        }
     }
-    const int n_kt = hi - lo;
+    const int n_kt = hi - lo + n_s;
+    auto key_tile = [&](int g) -> int { return kSink && g < n_s ? g : lo + g - (kSink ? n_s : 0); };
 
     const uint32_t tmem = tc_setup<C>(smem, sbase);
 
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                             b * p.Hq + hq);
             }
             for (int g = 0; g < n_kt; ++g) {
-                const int kv0 = (lo + g) * TB;
+                const int kv0 = key_tile(g) * TB;
                 const int ks = g % C::NK, ku = g / C::NK, vs = g % C::NV, vu = g / C::NV;
                 if (!in_range(box_ok(0, kv0, b * p.Hkv + hkv, D, p.Sk, (long long)p.B * p.Hkv, TB) &&
                                   kv0 >= 0 && kv0 < p.Sk,
@@ -716,11 +728,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             tc_fence_after();
             const uint32_t t_s = trow + C::COL_S + (g & 1) * TB + cb;
-            const int kv0 = (lo + g) * TB;
+            const int kv0 = key_tile(g) * TB;
             int clo, chi;
             cols_of_query(p, i, kv0, k_end, q_end, clo, chi);
             clo -= cb;
             chi -= cb;
+            const int cs = p.sinks - kv0 - cb;  // kSink: columns below it are sinks
             float pr[64];
             {
                 uint32_t sv[2][32];
@@ -738,8 +751,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                                      sl2x2, nl2),
                               x0, x1);
                     const float v0 = fast_exp2(x0), v1 = fast_exp2(x1);
-                    pr[x] = (x >= clo && x < chi) ? v0 : 0.f;
-                    pr[x + 1] = (x + 1 >= clo && x + 1 < chi) ? v1 : 0.f;
+                    pr[x] = ((x >= clo || (kSink && x < cs)) && x < chi) ? v0 : 0.f;
+                    pr[x + 1] = ((x + 1 >= clo || (kSink && x + 1 < cs)) && x + 1 < chi) ? v1 : 0.f;
                 }
             }
             if (!warp_wait(bar(C::BAR_DPFULL), g & 1, abort_flag, p.wait_limit_ns, p.status)) {
@@ -813,7 +826,7 @@ SideStream *side_stream() {
     return per_dev[dev];
 }
 
-template <int D>
+template <int D, bool kSink>
 attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     using C = TcCfg<D>;
     CUtensorMap tq, tk, tv, tdo;
@@ -822,8 +835,8 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     if ((st = make_tmap_bf16_3d(&tdo, a.dO, D, a.Sq, (uint64_t)a.B * a.Hq, TB)) != ATTN_OK) return st;
     if ((st = make_tmap_bf16_3d(&tk, a.K, D, a.Sk, (uint64_t)a.B * a.Hkv, TB)) != ATTN_OK) return st;
     if ((st = make_tmap_bf16_3d(&tv, a.V, D, a.Sk, (uint64_t)a.B * a.Hkv, TB)) != ATTN_OK) return st;
-    if (kernel_setup(reinterpret_cast<const void *>(bwd_dkdv_tc_kernel<D>), C::SMEM) != cudaSuccess ||
-        kernel_setup(reinterpret_cast<const void *>(bwd_dq_tc_kernel<D>), DqCfg<D>::SMEM) !=
+    if (kernel_setup(reinterpret_cast<const void *>(bwd_dkdv_tc_kernel<D, kSink>), C::SMEM) != cudaSuccess ||
+        kernel_setup(reinterpret_cast<const void *>(bwd_dq_tc_kernel<D, kSink>), DqCfg<D>::SMEM) !=
             cudaSuccess)
         return ATTN_ERR_CUDA;
     TcParams p;
@@ -845,6 +858,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     p.causal = a.causal;
     p.window = a.window;
     p.input_pos = a.input_pos;
+    p.sinks = a.sinks;
     p.wait_limit_ns = kWaitLimitNs;
     p.status = device_status_word();
     if (!p.status) return ATTN_ERR_CUDA;
@@ -859,13 +873,13 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     if (cudaEventRecord(ss->fork, stream) != cudaSuccess ||
         cudaStreamWaitEvent(ss->s, ss->fork, 0) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    bwd_dq_tc_kernel<D><<<static_cast<unsigned>(grid), kThreadsTc, DqCfg<D>::SMEM, ss->s>>>(tq, tk, tv, tdo, p,
+    bwd_dq_tc_kernel<D, kSink><<<static_cast<unsigned>(grid), kThreadsTc, DqCfg<D>::SMEM, ss->s>>>(tq, tk, tv, tdo, p,
                                                                                     n_qt);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     if (a.Sk > 0) {
         const long long grid_kv = (long long)((a.Sk + TB - 1) / TB) * a.Hkv * a.B;
         if (grid_kv > 0x7fffffffll) return ATTN_ERR_INVALID;
-        bwd_dkdv_tc_kernel<D><<<static_cast<unsigned>(grid_kv), kThreadsTc, C::SMEM, stream>>>(
+        bwd_dkdv_tc_kernel<D, kSink><<<static_cast<unsigned>(grid_kv), kThreadsTc, C::SMEM, stream>>>(
             tq, tk, tv, tdo, p);
         if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     }
@@ -878,8 +892,13 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
 }  // namespace
 
 attn_status_t launch_bwd_tc(const BwdArgs &a, cudaStream_t stream) {
-    if (a.D == 128) return launch_bwd_tc_d<128>(a, stream);
-    if (a.D == 64) return launch_bwd_tc_d<64>(a, stream);
+    if (a.sinks > 0) {
+        if (a.D == 128) return launch_bwd_tc_d<128, true>(a, stream);
+        if (a.D == 64) return launch_bwd_tc_d<64, true>(a, stream);
+        return ATTN_ERR_UNSUPPORTED;
+    }
+    if (a.D == 128) return launch_bwd_tc_d<128, false>(a, stream);
+    if (a.D == 64) return launch_bwd_tc_d<64, false>(a, stream);
     return ATTN_ERR_UNSUPPORTED;
 }
 

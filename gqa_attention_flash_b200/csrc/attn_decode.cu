@@ -26,6 +26,12 @@
 // half the copies of two 64-column boxes, 707 -> 674 us on the B64 paged workload
 // with 16-token blocks, bitwise the same.
 //
+// Sliding window with sinks (attn_decode_sinks, attn_decode_paged_sinks): the query is
+// the sequence's last token, so it sees the last `window` keys and the first `sinks`.
+// The slices then divide the 64-key tiles that hold such a key; chunks of a paged tile
+// without one are not read (their pages may have been freed), and the V rows of keys
+// that are not visible are zeroed in shared memory before they meet their zero weights.
+//
 // Kernel 2 (combine): one warp per (sequence, query head) merges the slices:
 // LSE = log sum_s exp(lse_s), O = sum_s exp(lse_s - LSE) o_s; empty slices
 // (lse = -inf) weigh nothing, and a sequence with no valid key gets O = 0.
@@ -72,6 +78,24 @@ struct DecParams {
     // paged cache only
     const int32_t *block_tables;  // (B, max_blocks)
     int max_blocks, block_shift, num_blocks, box_rows;
+    int window, sinks;  // kSink only
+};
+
+// The keys that the last of `len` tokens sees, key < sinks or key >= win_lo, and the
+// 64-key tiles that hold one: [0, n_sink) and [win_tile, n_all).
+struct SinkRange {
+    int win_lo, sinks, n_sink, win_tile, n_vis;
+    __device__ __forceinline__ SinkRange(int len, int window, int sinks_) {
+        win_lo = max(len - window, 0);
+        sinks = min(sinks_, len);
+        win_tile = win_lo / TN;
+        n_sink = min((sinks + TN - 1) / TN, win_tile);
+        n_vis = n_sink + (len + TN - 1) / TN - win_tile;
+    }
+    __device__ __forceinline__ int tile(int v) const { return v < n_sink ? v : win_tile + v - n_sink; }
+    __device__ __forceinline__ bool sees(int key) const { return key < sinks || key >= win_lo; }
+    // a visible key in [key, key + n) below the length
+    __device__ __forceinline__ bool any(int key, int n) const { return key < sinks || key + n > win_lo; }
 };
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -104,7 +128,7 @@ __device__ __forceinline__ uint32_t swz_t(int row, int chunk) {
     }
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kSink>
 __global__ void __launch_bounds__(kDecThreads)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const DecParams p) {
@@ -138,10 +162,11 @@ __global__ void __launch_bounds__(kDecThreads)
         len = p.S_cap;
     }
     if (len < 0) len = 0;
-    const int n_all = (len + TN - 1) / TN;
+    const SinkRange vis(len, kSink ? p.window : len, kSink ? p.sinks : 0);
+    const int n_all = kSink ? vis.n_vis : (len + TN - 1) / TN;
     const int per = (n_all + p.n_splits - 1) / p.n_splits;
     const int k0 = split * per * TN;
-    const int k1 = min(k0 + per * TN, len);
+    const int k1 = kSink ? min(k0 + per * TN, n_all * TN) : min(k0 + per * TN, len);
 
     float *ws_base = p.ws + ((long long)(b * p.Hq + h0) * p.n_splits + split) * C::WS_STRIDE;
     const long long ws_head = (long long)p.n_splits * C::WS_STRIDE;
@@ -157,6 +182,8 @@ __global__ void __launch_bounds__(kDecThreads)
     }
     const int t_begin = k0 / TN;
     const int n_tiles = (k1 + TN - 1) / TN - t_begin;
+    // first key of the slice's tile `it`
+    auto tile_row = [&](int it) -> int { return (kSink ? vis.tile(t_begin + it) : t_begin + it) * TN; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NS; ++s) {
@@ -180,7 +207,7 @@ __global__ void __launch_bounds__(kDecThreads)
             int ids[kMaxChunks];
             auto load_ids = [&](int it2) {
                 if constexpr (kPaged) {
-                    const int row2 = (t_begin + it2) * TN;
+                    const int row2 = tile_row(it2);
                     const int n2 = (min(TN, len - row2) + p.box_rows - 1) / p.box_rows;
                     const int32_t *bt = p.block_tables + (long long)b * p.max_blocks;
 #pragma unroll
@@ -195,7 +222,7 @@ __global__ void __launch_bounds__(kDecThreads)
                 if (use > 0 &&
                     !mbar_wait(empty(st), (use - 1) & 1, abort_flag, p.wait_limit_ns, p.status))
                     break;
-                const int row = (t_begin + it) * TN;
+                const int row = tile_row(it);
                 if constexpr (!kPaged) {
                     if (!in_range(box_ok(0, row, b * p.Hkv + hkv, D, p.S_cap, (long long)p.B * p.Hkv,
                                          TN) &&
@@ -220,11 +247,17 @@ __global__ void __launch_bounds__(kDecThreads)
 #pragma unroll
                     for (int k = 0; k < kMaxChunks; ++k) cur[k] = ids[k];
                     if (it + 1 < n_tiles) load_ids(it + 1);
-                    mbar_arrive_expect_tx(full(st), 2 * n_chunks * br * 128 * C::NBOX);
+                    int n_read = n_chunks;
+                    if constexpr (kSink) {
+                        n_read = 0;
+                        for (int k = 0; k < n_chunks; ++k) n_read += vis.any(row + k * br, br) ? 1 : 0;
+                    }
+                    mbar_arrive_expect_tx(full(st), 2 * n_read * br * 128 * C::NBOX);
 #pragma unroll
                     for (int k = 0; k < kMaxChunks; ++k) {
                         if (k >= n_chunks) break;
                         const int j = row + k * br;
+                        if (kSink && !vis.any(j, br)) continue;
                         const int blk = cur[k];
                         if (blk < 0 || blk >= p.num_blocks) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
                         // an out-of-range block reads as zeros (outside the tensor map)
@@ -281,8 +314,9 @@ __global__ void __launch_bounds__(kDecThreads)
                 ok = false;
                 break;
             }
-            const int key0 = (t_begin + it) * TN + warp * 16;  // first key of this warp
-            if (key0 < k1) {
+            const int key0 = tile_row(it) + warp * 16;  // first key of this warp
+            const int key_end = kSink ? len : k1;
+            if (key0 < key_end) {
                 const uint32_t kb = sbase + C::OFF_K + st * C::TILE;
                 const uint32_t vb = sbase + C::OFF_V + st * C::TILE;
                 // ---- S = Q K^T over this warp's 16 keys ----
@@ -304,7 +338,8 @@ __global__ void __launch_bounds__(kDecThreads)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int key = key0 + nb * 8 + 2 * t + (e & 1);
-                        const float x = key < k1 ? sc[nb][e] * p.scale_log2 : neg_inf();
+                        const bool seen = key < key_end && (!kSink || vis.sees(key));
+                        const float x = seen ? sc[nb][e] * p.scale_log2 : neg_inf();
                         sc[nb][e] = x;
                         mt[e >> 1] = fmaxf(mt[e >> 1], x);
                     }
@@ -341,12 +376,14 @@ __global__ void __launch_bounds__(kDecThreads)
                 pa[3] = pack_bf16x2(pr[1][2], pr[1][3]);
                 // Cache rows at or past the sequence length may hold anything; their
                 // weights are 0, but 0 * NaN is NaN, so zero this warp's such V rows.
-                const bool tail = key0 + 16 > len && key0 < p.S_cap;
+                // With a window, neither do the rows between the sinks and the window.
+                const bool cut = kSink && key0 < vis.win_lo && key0 + 16 > vis.sinks;
+                const bool tail = (key0 + 16 > len && key0 < p.S_cap) || cut;
                 if (tail) {
                     const int rows_from = max(len - key0, 0);
                     for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
                         const int rrow = idx / (D / 8), ch = idx % (D / 8);
-                        if (rrow >= rows_from)
+                        if (rrow >= rows_from || (kSink && !vis.sees(key0 + rrow)))
                             *reinterpret_cast<uint4 *>(smem + C::OFF_V + st * C::TILE +
                                                        swz_t<kWide>(warp * 16 + rrow, ch)) =
                                 make_uint4(0, 0, 0, 0);
@@ -470,7 +507,7 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kSink>
 attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     using C = DecCfg<D>;
     CUtensorMap tk, tv;
@@ -491,7 +528,7 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
         if ((st = make_tmap_bf16_3d(&tv, a.V, D, a.S_cap, (uint64_t)a.B * a.Hkv, TN)) != ATTN_OK)
             return st;
     }
-    if (kernel_setup(reinterpret_cast<const void *>(decode_split_kernel<D, kPaged>), C::SMEM_BYTES) !=
+    if (kernel_setup(reinterpret_cast<const void *>(decode_split_kernel<D, kPaged, kSink>), C::SMEM_BYTES) !=
         cudaSuccess)
         return ATTN_ERR_CUDA;
     DecParams p;
@@ -510,6 +547,8 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     if (!p.status) return ATTN_ERR_CUDA;
     p.block_tables = a.block_tables;
     p.max_blocks = a.max_blocks;
+    p.window = a.window;
+    p.sinks = a.sinks;
     p.num_blocks = a.num_blocks;
     p.box_rows = static_cast<int>(box_rows);
     p.block_shift = 0;
@@ -526,7 +565,7 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, decode_split_kernel<D, kPaged>, tk, tv, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, decode_split_kernel<D, kPaged, kSink>, tk, tv, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
     const int BH = a.B * a.Hq;
     cfg.gridDim = dim3((BH + 3) / 4, 1, 1);
@@ -546,13 +585,17 @@ size_t decode_workspace_floats(int B, int Hq, int n_splits, int D) {
 
 attn_status_t launch_decode(const DecodeArgs &a, cudaStream_t stream) {
     if (a.B == 0) return ATTN_OK;
-    if (a.block_tables) {
-        if (a.D == 128) return launch_decode_d<128, true>(a, stream);
-        if (a.D == 64) return launch_decode_d<64, true>(a, stream);
-        return ATTN_ERR_UNSUPPORTED;
-    }
-    if (a.D == 128) return launch_decode_d<128, false>(a, stream);
-    if (a.D == 64) return launch_decode_d<64, false>(a, stream);
+#define GQA_LAUNCH(DD)                                                         \
+    do {                                                                       \
+        if (a.window > 0)                                                      \
+            return a.block_tables ? launch_decode_d<DD, true, true>(a, stream) \
+                                  : launch_decode_d<DD, false, true>(a, stream); \
+        return a.block_tables ? launch_decode_d<DD, true, false>(a, stream)    \
+                              : launch_decode_d<DD, false, false>(a, stream);  \
+    } while (0)
+    if (a.D == 128) GQA_LAUNCH(128);
+    if (a.D == 64) GQA_LAUNCH(64);
+#undef GQA_LAUNCH
     return ATTN_ERR_UNSUPPORTED;
 }
 

@@ -114,6 +114,7 @@ struct FwdParams {
     int n_split;       // the last n_split pair items run as two single-tile items each
     float scale_log2;  // scale * log2(e)
     int causal, window, input_pos;
+    int sinks;         // keys j < sinks stay visible outside the window (kSink only)
     uint64_t wait_limit_ns;
     int *status;  // device status word
     // flex_attention! (read only by the flex instantiation)
@@ -191,16 +192,39 @@ struct FwdItem {
     int u_lo, u_hi, n_u;     // KV tiles the item loads (union of both ranges)
     bool act0, act1;         // query tile t sees at least one key
     bool rev;                // KV tiles visited last to first (ALiBi, negative slope)
+    // kSink: query tile t also sees KV tiles [0, s_t), s_t <= lo_t (the tiles of the
+    // sinks below its window); the item loads [0, s_u) and then [u_lo, u_hi)
+    int s0, s1, s_u;
 };
 
+template <bool kSink>
 __device__ __forceinline__ bool item_uses(const FwdItem &it, int t, int u) {
+    if constexpr (kSink) {
+        if (u < (t ? it.s1 : it.s0)) return true;
+    }
     return t ? (u >= it.lo1 && u < it.hi1) : (u >= it.lo0 && u < it.hi0);
+}
+
+// kSink: index of KV tile u among the tiles that query tile t visits.
+__device__ __forceinline__ int item_index(const FwdItem &it, int t, int u) {
+    const int s = t ? it.s1 : it.s0;
+    return u < s ? u : s + u - (t ? it.lo1 : it.lo0);
+}
+
+// KV tile of load index g of the item, and the reverse (increasing order).
+template <bool kSink>
+__device__ __forceinline__ int item_tile(const FwdItem &it, int g) {
+    return kSink && g < it.s_u ? g : it.u_lo + g - (kSink ? it.s_u : 0);
+}
+template <bool kSink>
+__device__ __forceinline__ int item_load(const FwdItem &it, int u) {
+    return kSink && u < it.s_u ? u : u - it.u_lo + (kSink ? it.s_u : 0);
 }
 
 // Work item w, in launch order: heaviest causal query-tile pairs first, the query
 // heads of one KV group adjacent (they share K/V through L2).  Step a1: the
 // visible KV tile range of each query tile (whole-tile skipping).
-template <int kMode>
+template <int kMode, bool kSink>
 __device__ __forceinline__ void fwd_item(const FwdParams &p, int w, FwdItem &it, bool report) {
     // The last n_split pair items of the launch order are split in two: item
     // n_full + 2 x + h is query tile h of pair item n_full + x.
@@ -242,7 +266,7 @@ __device__ __forceinline__ void fwd_item(const FwdParams &p, int w, FwdItem &it,
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
         const int q0 = (it.qt0 + t) * BM;
-        int lo_t = 0, hi_t = 0, qlast = q0;
+        int lo_t = 0, hi_t = 0, s_t = 0, qlast = q0;
         if (q0 < q_end && k_end > 0 && !(t == 1 && it.single)) {
             qlast = min(q0 + BM - 1, q_end - 1);
             long long hi = k_end;
@@ -253,15 +277,32 @@ __device__ __forceinline__ void fwd_item(const FwdParams &p, int w, FwdItem &it,
                 lo_t = static_cast<int>(lo / BN);
                 hi_t = static_cast<int>((hi + BN - 1) / BN);
             }
+            if constexpr (kSink) {
+                // tiles of the sinks below the window (all of them when the keys end
+                // before the window begins, which leaves the window's range empty)
+                s_t = static_cast<int>((min(hi, (long long)p.sinks) + BN - 1) / BN);
+                if (hi > lo) s_t = min(s_t, lo_t);
+                else lo_t = hi_t = s_t;
+            }
         }
-        if (t == 0) { it.lo0 = lo_t; it.hi0 = hi_t; it.ql0 = qlast; }
-        else { it.lo1 = lo_t; it.hi1 = hi_t; it.ql1 = qlast; }
+        if (t == 0) { it.lo0 = lo_t; it.hi0 = hi_t; it.ql0 = qlast; it.s0 = s_t; }
+        else { it.lo1 = lo_t; it.hi1 = hi_t; it.ql1 = qlast; it.s1 = s_t; }
     }
     it.act0 = it.hi0 > it.lo0;
     it.act1 = it.hi1 > it.lo1;
     it.u_lo = it.act0 ? (it.act1 ? min(it.lo0, it.lo1) : it.lo0) : it.lo1;
     it.u_hi = it.act0 ? (it.act1 ? max(it.hi0, it.hi1) : it.hi0) : it.hi1;
     it.n_u = (it.act0 || it.act1) ? it.u_hi - it.u_lo : 0;
+    if constexpr (kSink) {
+        it.s_u = max(it.s0, it.s1);
+        if (it.n_u > 0) {  // tiles below s_u are loaded once, with the sinks
+            it.u_lo = max(it.u_lo, it.s_u);
+            it.n_u = max(it.u_hi - it.u_lo, 0);
+        }
+        it.n_u += it.s_u;
+        it.act0 = it.act0 || it.s0 > 0;
+        it.act1 = it.act1 || it.s1 > 0;
+    }
     // AliBiScore with a negative slope: the bias grows towards the query, so the
     // KV tiles are visited nearest first; the running max is then found at once
     // and the lazy rescale of O stays rare.  (The softmax does not depend on the
@@ -280,7 +321,12 @@ __device__ __forceinline__ void fwd_item(const FwdParams &p, int w, FwdItem &it,
 // control), in launch order, so about one CTA per SM runs and the next item's Q
 // and first K/V tiles load and its first S products run while the current item
 // finishes.  Every barrier phase below is counted across items.
-template <int D, int kMode, bool kList>
+//
+// kSink (attn_fwd_sinks): keys j < sinks stay visible to the rows at or past them
+// whatever the window.  A query tile then visits the KV tiles of the sinks below its
+// window first and the window's tiles after them: one 128-key tile more per query
+// tile for up to 128 sinks.
+template <int D, int kMode, bool kList, bool kSink>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -335,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (kList) {
-        fwd_item<kMode>(p, blockIdx.x, it, false);
+        fwd_item<kMode, kSink>(p, blockIdx.x, it, false);
         // The KV tiles this CTA visits: inside a query tile's analytic range and
         // holding a visible block (BlockMask of flex_attention!), in order.
         if (warp == kWarpTma) {
@@ -346,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int u = base + lane;
                 uint32_t e = 0;
                 if (u < it.u_hi) {
-                    const uint32_t s0 = item_uses(it, 0, u) ? flex_states(p, bm, it.qt0, u) : 0u;
+                    const uint32_t s0 = item_uses<kSink>(it, 0, u) ? flex_states(p, bm, it.qt0, u) : 0u;
                     const uint32_t s1 =
-                        item_uses(it, 1, u) ? flex_states(p, bm, it.qt0 + 1, u) : 0u;
+                        item_uses<kSink>(it, 1, u) ? flex_states(p, bm, it.qt0 + 1, u) : 0u;
                     if (s0 | s1) e = static_cast<uint32_t>(u) | (s0 << 16) | (s1 << 24);
                 }
                 const uint32_t vote = __ballot_sync(0xffffffffu, e != 0);
@@ -407,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) {
       regs_dec<kProducerRegs>();
-      fwd_item<kMode>(p, blockIdx.x, it, false);
+      fwd_item<kMode, kSink>(p, blockIdx.x, it, false);
       if (warp == kWarpTma) {
         // ===================== TMA producer and work scheduler =====================
         if (lane == 0) {
@@ -456,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return false;
                     const int kv_row =
                         (kList ? static_cast<int>(kv_list[1 + g] & 0xFFFFu)
-                               : (it.rev ? it.u_hi - 1 - g : it.u_lo + g)) * BN;
+                               : (it.rev ? it.u_hi - 1 - g : item_tile<kSink>(it, g))) * BN;
                     // checked build: the K / V tile lies inside K and V
                     if (!in_range(box_ok(0, kv_row, it.b * p.Hkv + it.hkv, D, p.Sk,
                                          (long long)p.B * p.Hkv, BN) &&
@@ -506,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 item_slot[cs] = ok ? wn : -1;
                 mbar_arrive(bar(C::BAR_IFULL + cs));
                 if (!ok || wn < 0) break;
-                fwd_item<kMode>(p, wn, it, false);
+                fwd_item<kMode, kSink>(p, wn, it, false);
             }
         }
       } else if (warp == kWarpMma) {
@@ -576,21 +622,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (!kList) {
                         // last KV tile of query tile t in visiting order
                         auto last_of = [&](int t, int u) -> bool {
+                            if constexpr (kSink) {  // no window tile: the last sink tile
+                                if (t ? it.hi1 == it.lo1 : it.hi0 == it.lo0)
+                                    return u == (t ? it.s1 : it.s0) - 1;
+                            }
                             return it.rev ? u == (t ? it.lo1 : it.lo0) : u == (t ? it.hi1 : it.hi0) - 1;
                         };
-                        const int u_first = it.rev ? it.u_hi - 1 : it.u_lo;
+                        const int u_first = it.rev ? it.u_hi - 1 : item_tile<kSink>(it, 0);
 #pragma unroll
                         for (int t = 0; t < kTiles; ++t)
-                            if (ok && item_uses(it, t, u_first)) ok = issue_s(t, 0, last_of(t, u_first));
+                            if (ok && item_uses<kSink>(it, t, u_first)) ok = issue_s(t, 0, last_of(t, u_first));
                         for (int g = 0; ok && g < it.n_u; ++g) {
-                            const int u = it.rev ? it.u_hi - 1 - g : it.u_lo + g;
-                            const int un = it.rev ? u - 1 : u + 1;
+                            const int u = it.rev ? it.u_hi - 1 - g : item_tile<kSink>(it, g);
+                            const int un = it.rev ? u - 1 : (kSink ? item_tile<kSink>(it, g + 1) : u + 1);
 #pragma unroll
                             for (int t = 0; t < kTiles; ++t) {
-                                if (ok && item_uses(it, t, u))
+                                if (ok && item_uses<kSink>(it, t, u))
                                     ok = issue_pv(t, g, it.rev ? (t ? it.hi1 : it.hi0) - 1 - u
-                                                               : u - (t ? it.lo1 : it.lo0));
-                                if (ok && g + 1 < it.n_u && item_uses(it, t, un))
+                                                        : kSink ? item_index(it, t, u)
+                                                                : u - (t ? it.lo1 : it.lo0));
+                                if (ok && g + 1 < it.n_u && item_uses<kSink>(it, t, un))
                                     ok = issue_s(t, g + 1, last_of(t, un));
                             }
                             if (ok) mma_commit(bar(C::BAR_EMPTY + (gi + g) % C::NS));
@@ -626,14 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int wn = item_slot[k & 1];
                 mbar_arrive(bar(C::BAR_IEMPTY + (k & 1)));
                 if (wn < 0) break;
-                fwd_item<kMode>(p, wn, it, false);
+                fwd_item<kMode, kSink>(p, wn, it, false);
             }
         }
       }
     } else {
         // ===================== softmax / correction / epilogue =====================
         regs_inc<kSoftmaxRegs>();
-        fwd_item<kMode>(p, blockIdx.x, it, threadIdx.x == 0);
+        fwd_item<kMode, kSink>(p, blockIdx.x, it, threadIdx.x == 0);
         const int t = warp >> 2;                 // query tile of this warpgroup
         const int r = threadIdx.x & (BM - 1);    // row within the tile = TMEM lane
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -657,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this tile's range, selected without runtime-indexed arrays
             const int my_lo = t ? it.lo1 : it.lo0;
             const int my_hi = t ? it.hi1 : it.hi0;
+            const int my_s = kSink ? (t ? it.s1 : it.s0) : 0;
             const int my_qlast = t ? it.ql1 : it.ql0;
             const int k_end = it.k_end, q_end = it.q_end;
             float m_used = neg_inf();  // max subtracted so far (log2 units)
@@ -675,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // KV tiles of this query tile: its analytic range, or (flex) the listed
             // tiles whose block states for this query tile are not all 0.
             const int n_iter =
-                kList ? static_cast<int>(my_list[0]) : (my_hi > my_lo ? my_hi - my_lo : 0);
+                kList ? static_cast<int>(my_list[0]) : (my_hi > my_lo ? my_hi - my_lo : 0) + my_s;
             int n_done = 0;  // KV tiles this query tile has processed in this item
             for (int i = 0; i < n_iter; ++i) {
                 int u, g;  // KV tile and its load index within the item
@@ -688,9 +740,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     my_st = (e >> 20) & 0xFFu;
                     tile0_uses = (e >> 28) != 0;
                 } else {
-                    u = it.rev ? my_hi - 1 - i : my_lo + i;
-                    g = it.rev ? it.u_hi - 1 - u : u - it.u_lo;
-                    tile0_uses = item_uses(it, 0, u);
+                    u = it.rev ? my_hi - 1 - i : (kSink && i < my_s ? i : my_lo + i - my_s);
+                    g = it.rev ? it.u_hi - 1 - u : item_load<kSink>(it, u);
+                    tile0_uses = item_uses<kSink>(it, 0, u);
                 }
                 const int kv0 = u * BN;
                 if (!warp_wait(bar_s, (n_it + i) & 1, abort_flag, p.wait_limit_ns, p.status)) {
@@ -780,6 +832,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < BN; ++c)
                             s[c] = ((vm[c >> 5] >> (c & 31)) & 1u) ? s[c] : neg_inf();
+                    } else if constexpr (kSink) {
+                        const int c_s = min(p.sinks - kv0, BN);  // columns below it are sinks
+#pragma unroll
+                        for (int c = 0; c < BN; ++c)
+                            s[c] = ((c >= c_lo || c < c_s) && c < c_hi) ? s[c] : neg_inf();
                     } else {
 #pragma unroll
                         for (int c = 0; c < BN; ++c) s[c] = (c >= c_lo && c < c_hi) ? s[c] : neg_inf();
@@ -923,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::BAR_IEMPTY + (k & 1)));
             if (wn < 0) break;
-            fwd_item<kMode>(p, wn, it, false);
+            fwd_item<kMode, kSink>(p, wn, it, false);
         }
     }
 
@@ -938,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, int kMode, bool kList>
+template <int D, int kMode, bool kList, bool kSink = false>
 attn_status_t launch_fwd_d(const FwdArgs &a, cudaStream_t stream) {
     using C = FwdCfg<D, kList>;
     constexpr int kSmem = kList ? C::SMEM_BYTES_FLEX : C::SMEM_BYTES;
@@ -949,7 +1006,7 @@ attn_status_t launch_fwd_d(const FwdArgs &a, cudaStream_t stream) {
     if ((st = make_tmap_bf16_3d(&tv, a.V, D, a.Sk, (uint64_t)a.B * a.Hkv, BN)) != ATTN_OK) return st;
     // The register hand-over inside the kernel assumes exactly kLaunchRegs
     // registers per thread at launch; refuse to launch a build where it differs.
-    if (kernel_setup(reinterpret_cast<const void *>(attn_fwd_kernel<D, kMode, kList>), kSmem,
+    if (kernel_setup(reinterpret_cast<const void *>(attn_fwd_kernel<D, kMode, kList, kSink>), kSmem,
                      kLaunchRegs) != cudaSuccess)
         return ATTN_ERR_CUDA;
     FwdParams p;
@@ -981,6 +1038,7 @@ attn_status_t launch_fwd_d(const FwdArgs &a, cudaStream_t stream) {
     p.causal = a.causal;
     p.window = a.window;
     p.input_pos = a.input_pos;
+    p.sinks = a.sinks;
     p.wait_limit_ns = kWaitLimitNs;
     p.status = device_status_word();
     p.scale = a.scale;
@@ -1008,7 +1066,7 @@ attn_status_t launch_fwd_d(const FwdArgs &a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, kMode, kList>, tq, tk, tv, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, kMode, kList, kSink>, tq, tk, tv, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -1020,6 +1078,7 @@ attn_status_t launch_fwd(const FwdArgs &a, cudaStream_t stream) {
     const bool list = a.flex && (a.block_mask || a.doc_q);
 #define GQA_LAUNCH(DD)                                                            \
     do {                                                                          \
+        if (a.sinks > 0) return launch_fwd_d<DD, 0, false, true>(a, stream);      \
         if (list) {                                                               \
             if (mode == 0) return launch_fwd_d<DD, 0, true>(a, stream);           \
             if (mode == 2) return launch_fwd_d<DD, 2, true>(a, stream);           \

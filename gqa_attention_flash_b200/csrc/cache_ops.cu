@@ -1,0 +1,596 @@
+// cache_ops.cu -- operators on a paged KV cache: rows written to its pages and moved
+// inside them, pages copied, and the tables' bookkeeping (fork, extend, free).
+//
+// The cache is the one attn_decode_paged reads: pools (num_blocks, block_size, Hkv, D)
+// and tables int32 (R, max_blocks), row r of which names the pages of sequence r in
+// order (-1: no page).  The bookkeeping's state is ref_counts int32 (num_blocks): how
+// many table entries name a page.  A page is free when its count is 0, and the lowest
+// free pages are handed out first, so every result is a function of the inputs alone.
+//
+// All kernels are launched with programmatic dependent launch and wait for their
+// predecessor before the first global access.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace gqa {
+
+namespace {
+
+__device__ __forceinline__ void pdl_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... KArgs, typename... Args>
+attn_status_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) == cudaSuccess ? ATTN_OK
+                                                                                      : ATTN_ERR_CUDA;
+}
+
+// Pool row of position `pos` of the sequence whose table row is `bt`, or -1 (no page,
+// or a page outside the pool).
+__device__ __forceinline__ long long pool_row(const int32_t *bt, int pos, int shift, int num_blocks) {
+    const int p = bt[pos >> shift];
+    return p >= 0 && p < num_blocks ? ((long long)p << shift) + (pos & ((1 << shift) - 1)) : -1;
+}
+
+// ---------------------------------------------------------------------------------
+// append: row t of sequence b to position start[b] + t
+// ---------------------------------------------------------------------------------
+// One thread moves 16 bytes of K and of V.  The source's innermost axes are (t, d), so a
+// warp reads consecutive bytes and writes whole rows of one head (2 D bytes each).
+constexpr int kAppendThreads = 128;
+
+struct AppendParams {
+    uint4 *K, *V;
+    const uint4 *Kn, *Vn;
+    const int32_t *tables, *start, *n_new;
+    int Hkv, T, vec, max_blocks, shift, num_blocks, chunks;  // vec: 16-byte words per head row
+    long long capacity;
+    int *status;
+};
+
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+    pdl_wait();
+    const int chunk = static_cast<int>(blockIdx.x % p.chunks);
+    const long long bh = blockIdx.x / p.chunks;
+    const int h = static_cast<int>(bh % p.Hkv), b = static_cast<int>(bh / p.Hkv);
+    const long long idx = (long long)chunk * kAppendThreads + threadIdx.x;
+    const int t = static_cast<int>(idx / p.vec), c = static_cast<int>(idx % p.vec);
+    int n = p.T;
+    if (p.n_new) {
+        n = p.n_new[b];
+        if (n > p.T) {
+            record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+            n = p.T;
+        }
+    }
+    if (t >= n) return;
+    const long long pos = (long long)p.start[b] + t;
+    if (pos < 0 || pos >= p.capacity) {
+        record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const long long row =
+        pool_row(p.tables + (long long)b * p.max_blocks, static_cast<int>(pos), p.shift, p.num_blocks);
+    if (row < 0) {
+        record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const long long src = (bh * p.T + t) * p.vec + c, dst = (row * p.Hkv + h) * p.vec + c;
+    const uint4 k = p.Kn[src], v = p.Vn[src];
+    p.K[dst] = k;
+    p.V[dst] = v;
+}
+
+// ---------------------------------------------------------------------------------
+// compact: position base[b] + k takes the row of position base[b] + keep[b][k]
+// ---------------------------------------------------------------------------------
+// In place.  keep is ascending, so keep[k] >= k: a row that step k writes is the source
+// of no later step, and a block may move its slice of the columns in steps of kStep rows
+// (read the step, wait for the block, write it), with nothing but its own order to keep.
+constexpr int kCompactThreads = 256;
+constexpr int kSliceVec = 8;                                  // 16-byte words of a row per block
+constexpr int kStepRows = kCompactThreads / kSliceVec;        // rows per pass of the block
+constexpr int kPasses = 4;
+constexpr int kStep = kStepRows * kPasses;
+
+struct CompactParams {
+    uint4 *K, *V;
+    const int32_t *tables, *base, *keep, *n_keep;
+    int A, row_vec, slices, max_blocks, shift, num_blocks;  // row_vec: 16-byte words per token
+    long long capacity;
+    int *status;
+};
+
+__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactParams p) {
+    pdl_wait();
+    const int slice = static_cast<int>(blockIdx.x % p.slices);
+    const int b = static_cast<int>(blockIdx.x / p.slices);
+    uint4 *pool = blockIdx.y ? p.V : p.K;
+    const bool report = slice == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+    const int32_t *bt = p.tables + (long long)b * p.max_blocks;
+    const int32_t *keep = p.keep + (long long)b * p.A;
+    const long long base = p.base[b];
+    int n = p.A;
+    if (p.n_keep) {
+        n = p.n_keep[b];
+        if (n > p.A) {
+            if (report) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+            n = p.A;
+        }
+    }
+    if (n <= 0) return;
+    // The whole list is checked first: ascending, inside the table, on pages of the pool.
+    bool bad = base < 0;
+    for (int k = threadIdx.x; k < n && !bad; k += kCompactThreads) {
+        const int x = keep[k];
+        const int before = k > 0 ? keep[k - 1] : -1;
+        bad = x <= before || x < 0 || base + x >= p.capacity;
+        if (!bad)
+            bad = pool_row(bt, static_cast<int>(base + x), p.shift, p.num_blocks) < 0 ||
+                  pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks) < 0;
+    }
+    if (__syncthreads_or(bad)) {
+        if (report) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const int col = slice * kSliceVec + threadIdx.x % kSliceVec;
+    const int r = threadIdx.x / kSliceVec;
+    for (int k0 = 0; k0 < n; k0 += kStep) {
+        uint4 v[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int k = k0 + i * kStepRows + r;
+            if (k < n && col < p.row_vec)
+                v[i] = pool[pool_row(bt, static_cast<int>(base + keep[k]), p.shift, p.num_blocks) *
+                                p.row_vec + col];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int k = k0 + i * kStepRows + r;
+            if (k < n && col < p.row_vec)
+                pool[pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks) * p.row_vec + col] =
+                    v[i];
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// copy_blocks: page dst[i] takes the contents of page src[i]
+// ---------------------------------------------------------------------------------
+// Every block first looks through the list: a pair whose source is another pair's
+// destination, or whose destination a later pair names too, is skipped and flagged, so
+// the copies that run do not meet and the result does not depend on their order.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;
+
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_blocks_kernel(uint4 *K, uint4 *V, const int32_t *src, const int32_t *dst, int n, int num_blocks,
+                       long long page_vec, int chunks, int *status) {
+    pdl_wait();
+    const int i = static_cast<int>(blockIdx.x / chunks), chunk = static_cast<int>(blockIdx.x % chunks);
+    const int s = src[i], d = dst[i];
+    if (s < 0 || d < 0) return;  // no pair
+    bool bad = s >= num_blocks || d >= num_blocks;
+    for (int j = threadIdx.x; j < n && !bad; j += kCopyThreads)
+        if (j != i && src[j] >= 0) bad = dst[j] == s || (j > i && dst[j] == d);
+    if (__syncthreads_or(bad)) {
+        if (chunk == 0 && threadIdx.x == 0) record_status(status, ATTN_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    if (s == d) return;
+    const long long at = (long long)chunk * kCopyThreads * kCopyUnroll + threadIdx.x;
+    uint4 k[kCopyUnroll], v[kCopyUnroll];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+        const long long x = at + u * kCopyThreads;
+        if (x < page_vec) {
+            k[u] = K[s * page_vec + x];
+            v[u] = V[s * page_vec + x];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+        const long long x = at + u * kCopyThreads;
+        if (x < page_vec) {
+            K[d * page_vec + x] = k[u];
+            V[d * page_vec + x] = v[u];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// free: table entries [first, last) of the named rows
+// ---------------------------------------------------------------------------------
+constexpr int kTableThreads = 256;
+
+__global__ void __launch_bounds__(kTableThreads)
+    free_kernel(int32_t *tables, int32_t *refs, const int32_t *rows, const int32_t *first,
+                const int32_t *last, int R, int max_blocks, int num_blocks, int chunks, int *status) {
+    pdl_wait();
+    const int n = static_cast<int>(blockIdx.x / chunks), chunk = static_cast<int>(blockIdx.x % chunks);
+    const int row = rows[n];
+    if (row < 0) return;
+    if (row >= R) {
+        if (chunk == 0 && threadIdx.x == 0) record_status(status, ATTN_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const int k = chunk * kTableThreads + threadIdx.x;
+    if (k < first[n] || k >= last[n] || k >= max_blocks) return;
+    // taken out of the table at once, so that an entry named twice is given back once
+    const int page = atomicExch(&tables[(long long)row * max_blocks + k], -1);
+    if (page < 0) return;
+    if (page >= num_blocks) {
+        record_status(status, ATTN_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    if (atomicSub(&refs[page], 1) <= 0) {  // not held: put the count back
+        atomicAdd(&refs[page], 1);
+        record_status(status, ATTN_ERR_DEVICE_BOUNDS);
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// fork, first half: children's rows from their parents', shared pages counted
+// ---------------------------------------------------------------------------------
+// copy_src[n] is left at the parent's part-filled page (-1: none, or no such pair); the
+// second half gives the child a page of its own for it.
+struct ForkParams {
+    int32_t *tables, *refs, *lens;
+    const int32_t *parents, *children;
+    int32_t *copy_src, *copy_dst;
+    int N, R, max_blocks, num_blocks, shift, chunks;
+    int *status;
+};
+
+__device__ __forceinline__ int fork_len(const ForkParams &p, int row, bool report) {
+    const long long cap = (long long)p.max_blocks << p.shift;
+    const int len = p.lens[row];
+    if (len >= 0 && len <= cap) return len;
+    if (report) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    return len < 0 ? 0 : static_cast<int>(cap);
+}
+
+__global__ void __launch_bounds__(kTableThreads) fork_kernel(const ForkParams p) {
+    pdl_wait();
+    const int n = static_cast<int>(blockIdx.x / p.chunks), chunk = static_cast<int>(blockIdx.x % p.chunks);
+    const bool report = chunk == 0 && threadIdx.x == 0;
+    const int par = p.parents[n], chi = p.children[n];
+    bool bad = par >= p.R || chi >= p.R || par == chi;
+    const bool none = par < 0 || chi < 0;
+    for (int j = threadIdx.x; j < p.N && !bad && !none; j += kTableThreads)
+        if (p.parents[j] >= 0 && p.children[j] >= 0)
+            bad = p.parents[j] == chi || (j < n && p.children[j] == chi);
+    bad = __syncthreads_or(bad);
+    if (none || bad) {
+        if (report) {
+            p.copy_src[n] = -1;
+            if (!none) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+        }
+        return;
+    }
+    const int len = fork_len(p, par, report);
+    const int full = len >> p.shift;
+    const bool part = len & ((1 << p.shift) - 1);
+    const int32_t *from = p.tables + (long long)par * p.max_blocks;
+    int32_t *to = p.tables + (long long)chi * p.max_blocks;
+    const int k = chunk * kTableThreads + threadIdx.x;
+    if (k < p.max_blocks) {
+        int page = k < full ? from[k] : -1;
+        if (page >= p.num_blocks) {
+            record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+            page = -1;
+        }
+        if (page >= 0) atomicAdd(&p.refs[page], 1);
+        to[k] = page;
+    }
+    if (report) {
+        int page = part ? from[full] : -1;
+        if (page >= p.num_blocks) {
+            record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+            page = -1;
+        }
+        p.copy_src[n] = page < 0 ? -1 : page;
+        p.lens[chi] = len;
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// Handing out pages: fork's second half and extend
+// ---------------------------------------------------------------------------------
+constexpr int kAllocThreads = 1024;
+
+// Exclusive sum over the block; `total` gets the whole sum.
+__device__ __forceinline__ int block_exclusive(int v, int *warp_sums, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[31];
+    return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+// The first `need` free pages, in increasing order, into `list`; returns how many there
+// are (at most `need`).  Whole block.
+__device__ int free_pages(const int32_t *refs, int num_blocks, int need, int32_t *list, int *warp_sums) {
+    constexpr int kPer = 16;
+    int found = 0;
+    for (long long at = 0; at < num_blocks && found < need; at += kAllocThreads * kPer) {
+        const long long first = at + threadIdx.x * kPer;
+        uint32_t free_mask = 0;
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+            const long long x = first + 4 * q;
+            if (x + 4 <= num_blocks) {
+                const int4 r = *reinterpret_cast<const int4 *>(refs + x);
+                free_mask |= ((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << (4 * q);
+            } else {
+                for (int e = 0; e < 4; ++e)
+                    if (x + e < num_blocks && refs[x + e] == 0) free_mask |= 1u << (4 * q + e);
+            }
+        }
+        int total;
+        int rank = found + block_exclusive(__popc(free_mask), warp_sums, total);
+        while (free_mask && rank < need) {
+            list[rank++] = static_cast<int32_t>(first) + __ffs(free_mask) - 1;
+            free_mask &= free_mask - 1;
+        }
+        found += total;
+    }
+    __syncthreads();  // the list is complete, and refs[] may be written
+    return min(found, need);
+}
+
+// fork, second half: the k-th pair with a part-filled page gets the k-th free page.
+__global__ void __launch_bounds__(kAllocThreads) fork_alloc_kernel(const ForkParams p, int32_t *list) {
+    __shared__ int warp_sums[32];
+    pdl_wait();
+    int need = 0;
+    for (int n0 = 0; n0 < p.N; n0 += kAllocThreads) {
+        const int n = n0 + threadIdx.x;
+        int total;
+        block_exclusive(n < p.N && p.copy_src[n] >= 0, warp_sums, total);
+        need += total;
+    }
+    const int got = free_pages(p.refs, p.num_blocks, need, list, warp_sums);
+    if (got < need && threadIdx.x == 0) record_status(p.status, ATTN_ERR_NO_PAGES);
+    int before = 0;
+    for (int n0 = 0; n0 < p.N; n0 += kAllocThreads) {
+        const int n = n0 + threadIdx.x;
+        const bool mine = n < p.N && p.copy_src[n] >= 0;
+        int total;
+        const int rank = before + block_exclusive(mine, warp_sums, total);
+        before += total;
+        if (n < p.N) {
+            int page = -1;
+            if (mine && rank < got) {
+                page = list[rank];
+                const int full = fork_len(p, p.parents[n], false) >> p.shift;
+                p.tables[(long long)p.children[n] * p.max_blocks + full] = page;
+                p.refs[page] = 1;
+            }
+            p.copy_dst[n] = page;
+            if (page < 0) p.copy_src[n] = -1;
+        }
+    }
+}
+
+// extend: every empty entry of row r from position from_lens[r]'s page to the last page
+// that to_lens[r] tokens need gets a page, rows in order.
+struct ExtendParams {
+    int32_t *tables, *refs;
+    const int32_t *from, *to;
+    int32_t *offsets, *list;  // workspace: R + 1 and min(R * max_blocks, num_blocks)
+    int R, max_blocks, num_blocks, shift;
+    int *status;
+};
+
+__device__ __forceinline__ void extend_range(const ExtendParams &p, int r, bool report, int &k0, int &k1) {
+    const long long cap = (long long)p.max_blocks << p.shift;
+    long long to = p.to[r];
+    if (to > cap) {
+        if (report) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+        to = cap;
+    }
+    k0 = max(p.from[r], 0) >> p.shift;
+    k1 = to > 0 ? static_cast<int>((to + (1 << p.shift) - 1) >> p.shift) : 0;
+}
+
+__global__ void __launch_bounds__(kAllocThreads) extend_kernel(const ExtendParams p) {
+    __shared__ int warp_sums[32];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // empty entries of each row (a warp per row), then their exclusive sum over the rows
+    for (int r = warp; r < p.R; r += kAllocThreads / 32) {
+        int k0, k1, n = 0;
+        extend_range(p, r, lane == 0, k0, k1);
+        for (int k = k0 + lane; k < k1; k += 32) n += p.tables[(long long)r * p.max_blocks + k] < 0;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) p.offsets[r] = n;
+    }
+    __syncthreads();
+    long long need_all = 0;
+    for (int r0 = 0; r0 < p.R; r0 += kAllocThreads) {
+        const int r = r0 + threadIdx.x;
+        int total;
+        const int off = block_exclusive(r < p.R ? p.offsets[r] : 0, warp_sums, total);
+        if (r < p.R) p.offsets[r] = static_cast<int>(min(need_all + off, (long long)p.num_blocks));
+        need_all += total;
+    }
+    const int need = static_cast<int>(min(need_all, (long long)p.num_blocks));
+    if (need == 0) return;
+    const int got = free_pages(p.refs, p.num_blocks, need, p.list, warp_sums);
+    if (got < need_all && threadIdx.x == 0) record_status(p.status, ATTN_ERR_NO_PAGES);
+    for (int r = warp; r < p.R; r += kAllocThreads / 32) {
+        int k0, k1;
+        extend_range(p, r, false, k0, k1);
+        int rank = p.offsets[r];
+        for (int kb = k0; kb < k1; kb += 32) {
+            const int k = kb + lane;
+            int32_t *e = p.tables + (long long)r * p.max_blocks + k;
+            const bool empty = k < k1 && *e < 0;
+            const uint32_t vote = __ballot_sync(0xffffffffu, empty);
+            const int mine = rank + __popc(vote & ((1u << lane) - 1u));
+            if (empty && mine < got) {
+                const int page = p.list[mine];
+                *e = page;
+                p.refs[page] = 1;
+            }
+            rank += __popc(vote);
+        }
+    }
+}
+
+int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+}  // namespace
+
+attn_status_t launch_cache_append(const CacheArgs &a, cudaStream_t stream) {
+    AppendParams p;
+    p.K = static_cast<uint4 *>(a.K);
+    p.V = static_cast<uint4 *>(a.V);
+    p.Kn = static_cast<const uint4 *>(a.K_new);
+    p.Vn = static_cast<const uint4 *>(a.V_new);
+    p.tables = a.block_tables;
+    p.start = a.start;
+    p.n_new = a.counts;
+    p.Hkv = a.Hkv;
+    p.T = a.T;
+    p.vec = a.D / 8;
+    p.max_blocks = a.max_blocks;
+    p.shift = log2_of(a.block_size);
+    p.num_blocks = a.num_blocks;
+    p.capacity = (long long)a.max_blocks * a.block_size;
+    p.status = device_status_word();
+    if (!p.status) return ATTN_ERR_CUDA;
+    const long long chunks = ((long long)a.T * p.vec + kAppendThreads - 1) / kAppendThreads;
+    const long long grid = chunks * a.B * a.Hkv;
+    if (grid > 0x7fffffffll) return ATTN_ERR_INVALID;
+    p.chunks = static_cast<int>(chunks);
+    return launch_pdl(append_kernel, dim3(static_cast<unsigned>(grid)), kAppendThreads, 0, stream, p);
+}
+
+attn_status_t launch_cache_compact(const CacheArgs &a, cudaStream_t stream) {
+    CompactParams p;
+    p.K = static_cast<uint4 *>(a.K);
+    p.V = static_cast<uint4 *>(a.V);
+    p.tables = a.block_tables;
+    p.base = a.start;
+    p.keep = a.keep;
+    p.n_keep = a.counts;
+    p.A = a.T;
+    p.row_vec = a.Hkv * (a.D / 8);
+    p.slices = (p.row_vec + kSliceVec - 1) / kSliceVec;
+    p.max_blocks = a.max_blocks;
+    p.shift = log2_of(a.block_size);
+    p.num_blocks = a.num_blocks;
+    p.capacity = (long long)a.max_blocks * a.block_size;
+    p.status = device_status_word();
+    if (!p.status) return ATTN_ERR_CUDA;
+    const long long grid = (long long)p.slices * a.B;
+    if (grid > 0x7fffffffll) return ATTN_ERR_INVALID;
+    return launch_pdl(compact_kernel, dim3(static_cast<unsigned>(grid), 2), kCompactThreads, 0, stream, p);
+}
+
+attn_status_t launch_cache_copy(void *K, void *V, const int32_t *src, const int32_t *dst, int n,
+                                int num_blocks, long long page_bytes, cudaStream_t stream) {
+    int *status = device_status_word();
+    if (!status) return ATTN_ERR_CUDA;
+    const long long page_vec = page_bytes / 16;
+    const long long chunks = (page_vec + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
+    if (chunks * n > 0x7fffffffll) return ATTN_ERR_INVALID;
+    return launch_pdl(copy_blocks_kernel, dim3(static_cast<unsigned>(chunks * n)), kCopyThreads, 0, stream,
+                      static_cast<uint4 *>(K), static_cast<uint4 *>(V), src, dst, n, num_blocks, page_vec,
+                      static_cast<int>(chunks), status);
+}
+
+attn_status_t launch_cache_free(int32_t *tables, int32_t *refs, const int32_t *rows, const int32_t *first,
+                                const int32_t *last, int N, int R, int max_blocks, int num_blocks,
+                                cudaStream_t stream) {
+    int *status = device_status_word();
+    if (!status) return ATTN_ERR_CUDA;
+    const long long chunks = ((long long)max_blocks + kTableThreads - 1) / kTableThreads;
+    if (chunks * N > 0x7fffffffll) return ATTN_ERR_INVALID;
+    return launch_pdl(free_kernel, dim3(static_cast<unsigned>(chunks * N)), kTableThreads, 0, stream, tables,
+                      refs, rows, first, last, R, max_blocks, num_blocks, static_cast<int>(chunks), status);
+}
+
+attn_status_t launch_cache_fork(const CacheForkArgs &a, cudaStream_t stream) {
+    ForkParams p;
+    p.tables = a.tables;
+    p.refs = a.refs;
+    p.lens = a.lens;
+    p.parents = a.parents;
+    p.children = a.children;
+    p.copy_src = a.copy_src;
+    p.copy_dst = a.copy_dst;
+    p.N = a.N;
+    p.R = a.R;
+    p.max_blocks = a.max_blocks;
+    p.num_blocks = a.num_blocks;
+    p.shift = log2_of(a.block_size);
+    p.status = device_status_word();
+    if (!p.status) return ATTN_ERR_CUDA;
+    const long long chunks = ((long long)a.max_blocks + kTableThreads - 1) / kTableThreads;
+    if (chunks * a.N > 0x7fffffffll) return ATTN_ERR_INVALID;
+    p.chunks = static_cast<int>(chunks);
+    attn_status_t st = launch_pdl(fork_kernel, dim3(static_cast<unsigned>(chunks * a.N)), kTableThreads, 0,
+                                  stream, p);
+    if (st != ATTN_OK) return st;
+    return launch_pdl(fork_alloc_kernel, dim3(1), kAllocThreads, 0, stream, p, a.workspace);
+}
+
+attn_status_t launch_cache_extend(const CacheExtendArgs &a, cudaStream_t stream) {
+    ExtendParams p;
+    p.tables = a.tables;
+    p.refs = a.refs;
+    p.from = a.from;
+    p.to = a.to;
+    p.offsets = a.workspace;
+    p.list = a.workspace + a.R + 1;
+    p.R = a.R;
+    p.max_blocks = a.max_blocks;
+    p.num_blocks = a.num_blocks;
+    p.shift = log2_of(a.block_size);
+    p.status = device_status_word();
+    if (!p.status) return ATTN_ERR_CUDA;
+    return launch_pdl(extend_kernel, dim3(1), kAllocThreads, 0, stream, p);
+}
+
+}  // namespace gqa

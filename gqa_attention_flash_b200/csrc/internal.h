@@ -33,6 +33,9 @@ struct FwdArgs {
     int B, Hq, Hkv, Sq, Sk, D;
     float scale;
     int causal, window, input_pos;
+    // first keys that stay visible outside the window (attn_fwd_sinks); needs
+    // causal and window > 0, and excludes the flex extras
+    int sinks = 0;
     // flex_attention! extras; flex = 0 selects the plain kernel
     int flex = 0;
     float softcap = 0.f;
@@ -65,6 +68,9 @@ struct DecodeArgs {
     // Hkv, D) and S_cap = max_blocks * block_size
     const int32_t *block_tables = nullptr;
     int num_blocks = 0, block_size = 0, max_blocks = 0;
+    // sliding window with sinks (attn_decode_sinks): window > 0 keeps the last
+    // `window` keys and the first `sinks`; 0 = every key
+    int window = 0, sinks = 0;
 };
 
 // Backward of the forward (Tylo.jl `∇attention!`).
@@ -77,6 +83,7 @@ struct BwdArgs {
     float scale;
     int causal, window, input_pos;
     float *delta;  // workspace (B, Hq, Sq)
+    int sinks = 0;  // first keys that stay visible outside the window
 };
 
 attn_status_t launch_bwd(const BwdArgs &a, cudaStream_t stream);
@@ -95,6 +102,50 @@ struct RbsArgs {
 };
 
 attn_status_t launch_rbs(const RbsArgs &a, cudaStream_t stream);
+
+// Attention of T drafted tokens per sequence over a paged cache.
+struct TreeArgs {
+    void *O;
+    const void *Q, *K, *V;
+    const int32_t *block_tables, *context_lens, *parents, *draft_lens;
+    int B, Hq, Hkv, T, D;
+    int num_blocks, block_size, max_blocks;
+};
+attn_status_t launch_tree(const TreeArgs &a, cudaStream_t stream);
+
+// Operators on a paged cache (cache_ops.cu).
+struct CacheArgs {  // append and compact
+    void *K, *V;
+    const void *K_new = nullptr, *V_new = nullptr;
+    const int32_t *block_tables, *start, *counts, *keep = nullptr;
+    int B, Hkv, T, D;  // T: rows of K_new per sequence, or entries of keep
+    int num_blocks, block_size, max_blocks;
+};
+attn_status_t launch_cache_append(const CacheArgs &a, cudaStream_t stream);
+attn_status_t launch_cache_compact(const CacheArgs &a, cudaStream_t stream);
+attn_status_t launch_cache_copy(void *K, void *V, const int32_t *src, const int32_t *dst, int n,
+                                int num_blocks, long long page_bytes, cudaStream_t stream);
+
+struct CacheForkArgs {
+    int32_t *tables, *refs, *lens;
+    const int32_t *parents, *children;
+    int32_t *copy_src, *copy_dst;
+    int N, R, num_blocks, block_size, max_blocks;
+    int32_t *workspace;  // N ints
+};
+attn_status_t launch_cache_fork(const CacheForkArgs &a, cudaStream_t stream);
+
+struct CacheExtendArgs {
+    int32_t *tables, *refs;
+    const int32_t *from, *to;
+    int R, num_blocks, block_size, max_blocks;
+    int32_t *workspace;  // R + 1 + min(R * max_blocks, num_blocks) ints
+};
+attn_status_t launch_cache_extend(const CacheExtendArgs &a, cudaStream_t stream);
+
+attn_status_t launch_cache_free(int32_t *tables, int32_t *refs, const int32_t *rows, const int32_t *first,
+                                const int32_t *last, int N, int R, int max_blocks, int num_blocks,
+                                cudaStream_t stream);
 
 // Device address of the status word on the current device (looked up once per
 // device), or nullptr if the lookup failed.

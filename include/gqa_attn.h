@@ -41,7 +41,8 @@ typedef enum {
     ATTN_ERR_CUDA = 4,          /* a CUDA runtime / driver call failed */
     ATTN_ERR_TIMEOUT = 5,       /* device: a bounded wait ran out, kernel gave up */
     ATTN_ERR_DEVICE_BOUNDS = 6, /* device: a length exceeded the tensor, clamped */
-    ATTN_ERR_SCRATCH_LIMIT = 7  /* attn_decode_noalloc: workspace above its fixed array */
+    ATTN_ERR_SCRATCH_LIMIT = 7, /* attn_decode_noalloc: workspace above its fixed array */
+    ATTN_ERR_NO_PAGES = 8       /* device: no free page left in the cache's pool */
 } attn_status_t;
 
 /*
@@ -165,6 +166,33 @@ attn_status_t attn_bwd(void *dQ, void *dK, void *dV, const void *dO, const void 
                        const void *V, const void *O, const float *LSE, int B, int Hq, int Hkv,
                        int Sq, int Sk, int D, float scale, int causal, int window, int input_pos,
                        const int32_t *k_lengths, const int32_t *q_lengths, void *stream);
+
+/*
+ * attn_fwd_sinks -- attn_fwd_varlen with a sliding window and sinks: the first `sinks`
+ * keys stay visible to every query at or past them, whatever the window.
+ *
+ *   visible(i, j) = j <= p and (j > p - window or j < sinks),  p = input_pos + i,
+ *                   and j < k_lengths[b], i < q_lengths[b]
+ *
+ * Arguments, outputs and errors as attn_fwd_varlen with causal = 1, except that
+ * window >= 1 is required and sinks >= 0 is added.  sinks = 0 is attn_fwd_varlen with
+ * that window; a window of input_pos + Sq or more is plain causal attention.
+ */
+attn_status_t attn_fwd_sinks(void *O, const void *Q, const void *K, const void *V, float *LSE,
+                             int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                             int window, int sinks, int input_pos,
+                             const int32_t *k_lengths, const int32_t *q_lengths, void *stream);
+
+/*
+ * attn_bwd_sinks -- backward of attn_fwd_sinks: attn_bwd on that mask, with the same
+ * arguments, padding rules, workspace and errors (window >= 1, sinks >= 0, as in the
+ * forward).
+ */
+attn_status_t attn_bwd_sinks(void *dQ, void *dK, void *dV, const void *dO, const void *Q,
+                             const void *K, const void *V, const void *O, const float *LSE,
+                             int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                             int window, int sinks, int input_pos,
+                             const int32_t *k_lengths, const int32_t *q_lengths, void *stream);
 
 /*
  * attn_rbs_block_mask -- block scores and block mask of block-sparse prefill
@@ -301,6 +329,160 @@ attn_status_t attn_decode_paged(void *O, const void *Q, const void *K_cache, con
 attn_status_t attn_decode_noalloc(void *O, const void *Q, const void *K, const void *V,
                                   const int32_t *lengths, int n_splits, void *stream,
                                   int B, int Hq, int Hkv, int S_cap, int D);
+
+/*
+ * attn_decode_sinks, attn_decode_paged_sinks -- attn_decode and attn_decode_paged of a
+ * model with a sliding window and sinks.  The query is the last cached token, position
+ * lengths[b] - 1, so it sees the keys
+ *   j < lengths[b]  with  j >= lengths[b] - window  or  j < sinks.
+ * Cache rows of other keys are not read as values that reach O, whatever they hold; in
+ * the paged cache, entries of block_tables for pages without a visible key are not read
+ * either (attn_cache_free may have given them back).
+ * Arguments and errors as attn_decode / attn_decode_paged; window >= 1, sinks >= 0;
+ * n_splits 0..64, 0 = chosen by the library from the sizes.
+ */
+attn_status_t attn_decode_sinks(void *O, const void *Q, const void *K, const void *V,
+                                const int32_t *lengths, int window, int sinks, int n_splits,
+                                void *stream, int B, int Hq, int Hkv, int S_cap, int D);
+attn_status_t attn_decode_paged_sinks(void *O, const void *Q, const void *K_cache,
+                                      const void *V_cache, const int32_t *block_tables,
+                                      const int32_t *seq_lens, int window, int sinks,
+                                      int n_splits, void *stream, int B, int Hq, int Hkv,
+                                      int num_blocks, int block_size, int max_blocks_per_seq,
+                                      int D);
+
+/*
+ * attn_tree_paged -- attention of a tree of drafted tokens over a paged KV cache
+ * (speculative decoding: T drafts of each sequence checked in one pass).
+ *
+ *   O        [out] bf16 (B, Hq, T, D)
+ *   Q        [in]  bf16 (B, Hq, T, D)
+ *   K_cache, V_cache, block_tables [in] as attn_decode_paged.  The drafts' keys and values
+ *            already stand in the pages: draft i of sequence b at position
+ *            context_lens[b] + i (attn_cache_append writes them).
+ *   context_lens [in] int32 (B,): committed tokens of each sequence.
+ *   parents  [in] int32 (B, T): draft i continues draft parents[b][i], or the context
+ *            for -1.  Every parent comes before its child (-1 <= parents[b][i] < i).
+ *   draft_lens [in] int32 (B,) or NULL (= T): drafts i >= draft_lens[b] do not exist;
+ *            their rows of O are +0.0, whatever Q holds there.
+ *
+ * Draft i sees every key before context_lens[b], itself and its ancestors; scale is
+ * 1/sqrt(D).  A negative context length counts as 0; lengths past the table are clamped,
+ * a parent outside its range counts as -1, and a page outside the pool reads as zeros;
+ * each is flagged ATTN_ERR_DEVICE_BOUNDS.  Cache rows at or past context_lens[b] +
+ * draft_lens[b] never reach O; those before it must hold finite values.
+ *   Sizes: B >= 0; T 0..256; Hq, Hkv >= 1, Hq % Hkv == 0, Hq / Hkv <= 16;
+ *          block_size a power of two >= 8; D in {64, 128}.
+ */
+attn_status_t attn_tree_paged(void *O, const void *Q, const void *K_cache, const void *V_cache,
+                              const int32_t *block_tables, const int32_t *context_lens,
+                              const int32_t *parents, const int32_t *draft_lens, void *stream,
+                              int B, int Hq, int Hkv, int T, int num_blocks, int block_size,
+                              int max_blocks_per_seq, int D);
+
+/*
+ * Operators on a paged KV cache
+ * -----------------------------
+ * The cache is attn_decode_paged's: pools (num_blocks, block_size, Hkv, D) and
+ * block_tables int32 (R, max_blocks_per_seq), -1 where a sequence has no page.  A
+ * serving loop keeps one table and one ref_counts for all layers and one pair of pools
+ * per layer: append, compact and copy_blocks work on a layer's pools, fork, extend and
+ * free on the table.
+ *   ref_counts int32 (num_blocks): how many table entries name each page.  A page is
+ *   free when its count is 0; fork and extend hand out the lowest free pages first, so
+ *   their results depend on their arguments alone.
+ * block_size is a power of two >= 8, max_blocks_per_seq >= 1, num_blocks >= 1, and
+ * num_blocks * block_size and max_blocks_per_seq * block_size below 2^31.  Calls that
+ * share a table, counts or pages are to be ordered by the caller (one stream).
+ */
+
+/*
+ * attn_cache_append -- write new rows of keys and values to their pages.
+ *   K_new, V_new [in] bf16 (B, Hkv, T, D) (the layout attn_fwd reads)
+ *   start  [in] int32 (B,): row t of sequence b goes to position start[b] + t
+ *   n_new  [in] int32 (B,) or NULL (= T): rows t >= n_new[b] are not written.
+ * A row whose position lies outside the table, or on an entry without a page of the
+ * pool, is not written and flagged ATTN_ERR_DEVICE_BOUNDS, as is n_new[b] > T (clamped).
+ * Two rows of one call may not go to the same place (pages shared by two sequences).
+ */
+attn_status_t attn_cache_append(void *K_cache, void *V_cache, const void *K_new,
+                                const void *V_new, const int32_t *block_tables,
+                                const int32_t *start, const int32_t *n_new, void *stream,
+                                int B, int Hkv, int T, int num_blocks, int block_size,
+                                int max_blocks_per_seq, int D);
+
+/*
+ * attn_cache_compact -- move the rows that are kept to the front, in place: position
+ * base[b] + k takes the keys and values of position base[b] + keep[b][k],
+ * k < n_keep[b] (the accepted path of a tree of drafts; the rows a pruned cache keeps).
+ *   base   [in] int32 (B,)
+ *   keep   [in] int32 (B, A), strictly increasing, >= 0 over its first n_keep[b] entries
+ *   n_keep [in] int32 (B,) or NULL (= A); values above A are clamped and flagged.
+ * Rows past base[b] + n_keep[b] are left as they are.  A sequence whose list is not
+ * increasing, leaves the table, or touches an entry without a page of the pool is left
+ * untouched and flagged ATTN_ERR_DEVICE_BOUNDS.  Rows that two sequences share may not be
+ * moved.
+ */
+attn_status_t attn_cache_compact(void *K_cache, void *V_cache, const int32_t *block_tables,
+                                 const int32_t *base, const int32_t *keep,
+                                 const int32_t *n_keep, void *stream, int B, int Hkv, int A,
+                                 int num_blocks, int block_size, int max_blocks_per_seq, int D);
+
+/*
+ * attn_cache_copy_blocks -- page dst[i] takes the contents of page src[i], i < N, in both
+ * pools.  A pair with a negative entry is no pair.  A pair is skipped and flagged
+ * ATTN_ERR_DEVICE_BOUNDS when a page is outside the pool, when its source is another
+ * pair's destination, or when a later pair names the same destination.  N <= 65536.
+ */
+attn_status_t attn_cache_copy_blocks(void *K_cache, void *V_cache, const int32_t *src,
+                                     const int32_t *dst, void *stream, int N, int num_blocks,
+                                     int block_size, int Hkv, int D);
+
+/*
+ * attn_cache_fork -- sequences that continue others: row children[n] of the table becomes
+ * a copy of row parents[n] up to its length.  Whole pages are shared (their counts rise by
+ * one); a part-filled last page is not: the child gets a free page for it (count 1), and
+ * the pair of pages goes to copy_src[n], copy_dst[n] (-1, -1 without one), for
+ * attn_cache_copy_blocks on every layer.  The rest of the child's row is -1, and
+ * seq_lens[children[n]] = seq_lens[parents[n]].
+ *   block_tables [in/out] int32 (R, max_blocks_per_seq), ref_counts [in/out],
+ *   seq_lens [in/out] int32 (R,), parents, children [in] int32 (N,),
+ *   copy_src, copy_dst [out] int32 (N,).
+ * The child's row is overwritten: give back what it held first (attn_cache_free).  A pair
+ * with a negative entry is no pair.  A pair is skipped and flagged ATTN_ERR_DEVICE_BOUNDS
+ * when a row is outside the table, when its child is also a parent, or the child of an
+ * earlier pair.  Free pages go to the pairs in order; a pair that gets none keeps -1
+ * there and the call flags ATTN_ERR_NO_PAGES.  N <= 65536.
+ */
+attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_t *seq_lens,
+                              const int32_t *parents, const int32_t *children,
+                              int32_t *copy_src, int32_t *copy_dst, void *stream, int N, int R,
+                              int num_blocks, int block_size, int max_blocks_per_seq);
+
+/*
+ * attn_cache_extend -- pages for the next tokens: in each row r, the empty (negative)
+ * entries from the page of position from_lens[r] to the last page that to_lens[r] tokens
+ * need get free pages (count 1), rows in order, entries in order.  Entries that hold a
+ * page keep it.  to_lens[r] past the table is clamped and flagged
+ * ATTN_ERR_DEVICE_BOUNDS; entries for which no page is left stay as they are and the call
+ * flags ATTN_ERR_NO_PAGES.
+ *   block_tables, ref_counts [in/out], from_lens, to_lens [in] int32 (R,).
+ */
+attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts,
+                                const int32_t *from_lens, const int32_t *to_lens, void *stream,
+                                int R, int num_blocks, int block_size, int max_blocks_per_seq);
+
+/*
+ * attn_cache_free -- give back the pages of table entries first[n] .. last[n]-1 of row
+ * rows[n], n < N: the entries become -1 and their pages' counts fall by one (a whole
+ * sequence; the pages behind a rejected draft; those that left a sliding window).  Empty
+ * entries are passed over, ranges are cut to the table, and a negative row names none.
+ * A row or page out of range, or a page whose count is already 0 (which stays 0), is
+ * flagged ATTN_ERR_DEVICE_BOUNDS.
+ */
+attn_status_t attn_cache_free(int32_t *block_tables, int32_t *ref_counts, const int32_t *rows,
+                              const int32_t *first, const int32_t *last, void *stream, int N,
+                              int R, int num_blocks, int max_blocks_per_seq);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *attn_status_string(attn_status_t status);
