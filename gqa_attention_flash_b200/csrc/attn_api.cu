@@ -170,6 +170,21 @@ attn_status_t make_tmap_bf16_paged_wide(CUtensorMap *map, const void *base, uint
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID;
 }
 
+attn_status_t make_tmap_bf16_paged_groups(CUtensorMap *map, const void *base, uint64_t D, uint64_t heads,
+                                          uint64_t rows, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return ATTN_ERR_CUDA;
+    const cuuint64_t row = D * 2 * heads;  // bytes
+    const cuuint64_t dims[5] = {64, 8, D / 64, rows / 8, heads};
+    const cuuint64_t strides[4] = {row, 128, 8 * row, D * 2};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), box_rows / 8, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims,
+                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID;
+}
+
 namespace {
 
 __global__ void wait_probe_kernel(uint64_t limit_ns) {

@@ -25,6 +25,16 @@ attn_status_t make_tmap_bf16_paged(CUtensorMap *map, const void *base, uint64_t 
 attn_status_t make_tmap_bf16_paged_wide(CUtensorMap *map, const void *base, uint64_t heads,
                                         uint64_t rows, uint32_t box_rows);
 
+// The same cache (D = 64 or 128) viewed as 8-row groups: one box copies box_rows (a
+// multiple of 8) consecutive rows of one head, stored as (group, 64-column half, 8 rows,
+// 64 columns), each 8 x 128-byte block 128-byte swizzled.  Coordinates (0, 0, 0, group, head).
+attn_status_t make_tmap_bf16_paged_groups(CUtensorMap *map, const void *base, uint64_t D, uint64_t heads,
+                                          uint64_t rows, uint32_t box_rows);
+
+// Stream-ordered workspace from the library's pool on the current device (freed with
+// cudaFreeAsync on the same stream).
+cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream);
+
 struct FwdArgs {
     void *O;
     const void *Q, *K, *V;
