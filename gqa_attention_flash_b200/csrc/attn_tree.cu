@@ -646,13 +646,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // Rows of the segments that several CTAs worked on, from their partial states; rows of
-// sequences without a draft are zeroed here too.  One warp per row.
+// sequences without a draft are zeroed here too.  One warp per row: a lane per piece for the
+// weights, then D / 32 columns per lane over all pieces, whose loads do not depend on one
+// another (8 pieces a row: 28 -> 5 us for one sequence of 8 drafts against a loop that read
+// a piece's max before its row).
 constexpr int kCombineThreads = 256;
-constexpr int kCombineRows = 32;
 
 template <int D, bool kTwo>
 __global__ void __launch_bounds__(kCombineThreads)
-    tree_combine_kernel(const TreeParams p, int row_blocks) {
+    tree_combine_kernel(const TreeParams p, int row_blocks, int rows_per_block) {
     using C = TreeCfg<D, kTwo>;
     constexpr int PER = D / 32;
     __shared__ long long warp_sums[kCombineThreads / 32], found;
@@ -675,8 +677,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     const long long share = (total * H + p.n_cta - 1) / p.n_cta;
     const TreeLens len = tree_lens(p, b, false);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int k = warp; k < kCombineRows; k += kCombineThreads / 32) {
-        const int row = rb * kCombineRows + k;
+    for (int k = warp; k < rows_per_block; k += kCombineThreads / 32) {
+        const int row = rb * rows_per_block + k;
         if (row >= p.R) break;
         __nv_bfloat16 *out = p.O + ((long long)(b * p.Hq + hkv * (p.Hq / p.Hkv)) * p.T + row) * D + lane * PER;
         float acc[PER] = {};
@@ -684,28 +686,45 @@ __global__ void __launch_bounds__(kCombineThreads)
         if (len.nt > 0) {
             const int rt = row / C::ROWS, prow = row - rt * C::ROWS;
             const long long f0 = found * H + (long long)(hkv * p.n_rt + rt) * len.nt, f1 = f0 + len.nt;
-            const long long c0 = f0 / share, c1 = (f1 - 1) / share;
-            if (c0 == c1) continue;  // one CTA wrote the row
-            auto slot = [&](long long c) -> const float * {
-                return p.ws + (2 * c + (c == c0 && f0 > c0 * share ? 1 : 0)) * C::WS;
+            const int c0 = static_cast<int>(f0 / share), n = static_cast<int>((f1 - 1) / share) - c0 + 1;
+            if (n == 1) continue;  // one CTA wrote the row
+            const float *ws0 = p.ws + (long long)(2 * c0) * C::WS;
+            // piece i of the segment: slot 2 (c0 + i), or 2 c0 + 1 when it closes c0's run
+            const int odd = f0 > c0 * share ? 1 : 0;
+            auto piece = [&](int i) -> const float * {
+                return ws0 + (long long)(2 * i + (i == 0 ? odd : 0)) * C::WS;
             };
-            float M = ninf();
-            for (long long c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[C::ROWS * D + prow]);
+            float M = ninf(), lsum = 0.f;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                const bool has = i0 + lane < n;
+                const float *s = piece(has ? i0 + lane : 0) + C::ROWS * D + prow;
+                const float m = has ? s[0] : ninf(), l = has ? s[C::ROWS] : 0.f;
+                float top = m;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            float lsum = 0.f;
-            if (M != ninf()) {
-                for (long long c = c0; c <= c1; ++c) {
-                    const float *s = slot(c);
-                    const float m = s[C::ROWS * D + prow];
-                    if (m == ninf()) continue;
-                    const float wt = fast_exp2(m - M);
-                    lsum = fmaf(wt, s[C::ROWS * (D + 1) + prow], lsum);
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float grown = fmaxf(M, top);
+                if (grown == ninf()) continue;
+                const float old = fast_exp2(M - grown);  // 0 for the first batch
+                M = grown;
+                const float wt = fast_exp2(m - M);
+                lsum = lsum * old + wt * l;
 #pragma unroll
-                    for (int x = 0; x < PER; ++x)
-                        acc[x] = fmaf(wt, s[prow * D + lane * PER + x], acc[x]);
+                for (int x = 0; x < PER; ++x) acc[x] *= old;
+                const int cnt = min(32, n - i0);
+#pragma unroll 8
+                for (int i = 0; i < cnt; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, wt, i);
+                    const float *src = piece(i0 + i) + prow * D + lane * PER;
+                    float v[PER];
+                    if constexpr (PER == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src);
+                    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
+                    // a piece that saw no key of this row holds nothing to weigh
+#pragma unroll
+                    for (int x = 0; x < PER; ++x) acc[x] = wi > 0.f ? fmaf(wi, v[x], acc[x]) : acc[x];
                 }
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
             if (lsum > 0.f && row % p.T < len.drafts) inv = 1.f / lsum;
         }
 #pragma unroll
@@ -769,12 +788,16 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     st = cudaLaunchKernelEx(&cfg, tree_kernel<D, kTwo>, tq, tk, tv, p) == cudaSuccess ? ATTN_OK
                                                                                      : ATTN_ERR_CUDA;
-    const int row_blocks = (p.R + kCombineRows - 1) / kCombineRows;
+    // a row per warp while the blocks fit on the SMs at once, four where that leaves more
+    // blocks that only find their segment whole
+    const long long fine = ((long long)p.R + 7) / 8 * a.B * a.Hkv;
+    const int rows_per_block = fine <= 8ll * p.n_cta ? 8 : 32;
+    const int row_blocks = (p.R + rows_per_block - 1) / rows_per_block;
     if (st == ATTN_OK) {
         cfg.gridDim = dim3(static_cast<unsigned>(row_blocks) * a.B * a.Hkv, 1, 1);
         cfg.blockDim = dim3(kCombineThreads, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, kTwo>, p, row_blocks) != cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, kTwo>, p, row_blocks, rows_per_block) != cudaSuccess)
             st = ATTN_ERR_CUDA;
     }
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
@@ -786,7 +809,7 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream) {
 attn_status_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
     const int R = a.Hq / a.Hkv * a.T;
     if ((long long)a.B * a.Hq * a.T > 0x7fffffffll - 2 * TM ||
-        (long long)a.B * a.Hkv * ((R + kCombineRows - 1) / kCombineRows) > 0x7fffffffll)
+        (long long)a.B * a.Hkv * ((R + 31) / 32) > 0x7fffffffll)
         return ATTN_ERR_INVALID;
     if (a.D == 128) return R > TM ? launch_tree_d<128, true>(a, stream) : launch_tree_d<128, false>(a, stream);
     return R > TM ? launch_tree_d<64, true>(a, stream) : launch_tree_d<64, false>(a, stream);
