@@ -7,23 +7,25 @@
 //   O_i = softmax_j(<q_i, k_j> / sqrt(D)) V over j < ctx and j = ctx + a, a in anc(i).
 //
 // Rows.  The G T queries of a KV head (its G query heads, T drafts each) are consecutive
-// rows of Q, so they make the M = 128 rows of one or two MMA tiles and every K/V byte is
-// read from HBM once for up to 256 of them.  Up to 128 rows, one tile (kTwo = false): the
-// two softmax warpgroups take the even and the odd key tiles of the same rows and merge
-// their states at the end, so that one's softmax overlaps the other's products.  Above,
-// two tiles (kTwo) share every key tile, one warpgroup each; more rows take several passes.
+// rows of Q, so every K/V byte is read from HBM once for up to 256 of them.
+// Up to 128 rows, one M = 128 tile (kTwo = false): the two softmax warpgroups take the even
+// and the odd key tiles of the same rows and merge their states at the end, so that one's
+// softmax overlaps the other's products.  Above, two tiles (kTwo) share every key tile, one
+// warpgroup each; more rows take several passes.  Few rows leave most of the tile empty, but
+// the time is HBM's: transposed products (keys as M, N = 64 rows) halve the tensor work of
+// 64 rows and ran no faster (B64 x 16 drafts: 768 us against 732).
 //
 // Work.  The 128-key tiles of all (sequence, KV head, row pass) segments form one list
 // that the CTAs share out in equal runs, so ragged lengths leave no SM idle and a single
 // long sequence uses all of them.  A segment that ends up in several CTAs leaves partial
 // states (max, sum, unnormalised O, fp32) in a workspace; tree_combine_kernel merges them.
 //
-// 12 warps: 0-3 and 4-7 softmax (one row per thread = TMEM lane), 8 TMA producer, 9 MMA
-// issuer, 10-11 idle; registers move from 8-11 to the softmax warps as in the forward.
-// The producer gathers each key tile page by page into a ring of 128-row slots,
-// K and V in turn; a lane per page copies min(block_size, 128) rows of one head in one
-// 5-D TMA box whose shared-memory order is (8-row group, 64-column half, row, column), the
-// 128-byte-swizzled operand layout with 8-row groups 128 D / 64 * 8 bytes apart.
+// 12 warps: 0-3 and 4-7 softmax (one row per thread = TMEM lane), 8 and 10 TMA producers,
+// 9 MMA issuer, 11 idle; registers move from 8-11 to the softmax warps as in the forward.
+// The producers gather K and V page by page into a ring of 128-row slots each; a lane per
+// page copies min(block_size, 128) rows of one head in one 5-D TMA box whose shared-memory
+// order is (8-row group, 64-column half, row, column): the 128-byte-swizzled operand layout
+// with 8-row groups 1024 D / 64 bytes apart.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -40,21 +42,26 @@ constexpr int kTreeRegs = 168;  // per thread at launch (checked on the host)
 constexpr uint32_t kLoadRegs = 88, kSoftRegs = 208;
 static_assert(128 * kLoadRegs + 256 * kSoftRegs <= kTreeThreads * kTreeRegs,
               "register split must use exactly the launch allocation");
-constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10;
 constexpr int kMaxDrafts = 256;
 
 template <int D, bool kTwo>
 struct TreeCfg {
     static constexpr int NQ = kTwo ? 2 : 1;          // resident row tiles
+    static constexpr int RQ = TM;                    // rows of a Q tile
     static constexpr int NBOX = D / 64;
     static constexpr int TILE = TK * D * 2;          // one K, V or Q tile
-    static constexpr int QBOX = TM * 128;            // a Q tile's 64-column half
+    static constexpr int QTILE = RQ * D * 2;
+    static constexpr int QBOX = RQ * 128;            // a Q tile's 64-column half
     static constexpr int GROUP = NBOX * 1024;        // 8 rows of a K or V tile
-    static constexpr int NS = (D == 128 ? 7 : 13) - NQ;  // ring slots
+    // K and V slots, a ring each: every producer fills its own ring in order, so the parity
+    // that it waits for is never ambiguous
+    static constexpr int NS = (D == 128 ? 7 : 13) - NQ, NK = NS / 2, NV = NS - NK;
     static constexpr int ROWS = NQ * TM;             // rows of a segment
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = NQ * TILE;
     static constexpr int OFF_BAR = OFF_RING + NS * TILE;
+    // full and empty: [NK] slots of K, then [NV] of V
     static constexpr int BAR_FULL = 0, BAR_EMPTY = NS, BAR_QFULL = 2 * NS, BAR_QFREE = 2 * NS + 1,
                          BAR_S = 2 * NS + 2, BAR_P = 2 * NS + 4, BAR_O = 2 * NS + 6,
                          N_BARS = 2 * NS + 8;
@@ -181,6 +188,158 @@ struct TreeWalk {
     }
 };
 
+// Set-up shared by the kernels: barriers, this CTA's run of the list, TMEM.  False: the CTA
+// has no work (nothing is allocated then).
+template <class C>
+__device__ __forceinline__ bool tree_setup(const TreeParams &p, uint8_t *smem, TreeWalk &w, uint32_t &tmem) {
+    const uint32_t sbase = smem_u32(smem);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    int *abort_flag = reinterpret_cast<int *>(smem + C::OFF_MISC + 4);
+    int *first_b = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);
+    long long *first_pre = reinterpret_cast<long long *>(smem + C::OFF_ML);  // before the first piece
+    long long *warp_sums = first_pre + 1;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::N_BARS; ++i)
+            mbar_init(sbase + C::OFF_BAR + 8 * i, i == C::BAR_P || i == C::BAR_P + 1 ? TM : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    long long mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += tree_lens(p, b, blockIdx.x == 0).nt;
+    const long long before = block_scan(mine, warp_sums, total);
+    const long long H = (long long)p.Hkv * p.n_rt;
+    const long long share = (total * H + p.n_cta - 1) / p.n_cta;
+    w.f_first = w.f = blockIdx.x * share;
+    w.f_end = min(total * H, w.f + share);
+    if (w.f >= w.f_end) return false;
+    if (before * H <= w.f && w.f < (before + mine) * H) {
+        long long pre = before;
+        int b = b0;
+        for (;; ++b) {
+            const int nt = tree_lens(p, b, false).nt;
+            if (w.f < (pre + nt) * H) break;
+            pre += nt;
+        }
+        *first_b = b;
+        *first_pre = pre;
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem = *tmem_slot;
+    w.b = *first_b;
+    w.pre = *first_pre;
+    w.len = tree_lens(p, w.b, false);
+    __syncthreads();  // the exchange area is reused from here on
+    return true;
+}
+
+template <class C>
+__device__ __forceinline__ void tree_teardown(uint8_t *smem, uint32_t tmem) {
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    if (*abort_flag) drain_delay(2000000);  // let copies and MMAs in flight land
+    tc_fence_before();
+    __syncthreads();
+    if ((threadIdx.x >> 5) == kWarpMma) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Rows of tile t of the segment that exist.
+template <class C>
+__device__ __forceinline__ int tree_rows(const TreeParams &p, int rt, int t) {
+    return min(C::RQ, p.R - (rt * C::NQ + t) * C::RQ);
+}
+
+// TMA producers: warp 8 copies the pieces' Q tiles and K, warp 10 V, page by page.  A box
+// takes its warp about 28 ns to issue (the copy wants its operands in uniform registers, so
+// the lanes take turns): with 16-token pages one warp for both would need 0.45 us for a
+// 128-key tile, a third of the time its 64 KB take from HBM.
+template <int D, class C>
+__device__ __forceinline__ void tree_produce(const TreeParams &p, uint8_t *smem, TreeWalk &w,
+                                             bool is_v, const CUtensorMap *tmQ, const CUtensorMap *tmK,
+                                             const CUtensorMap *tmV) {
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8 * i; };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        prefetch_tensormap(tmQ);
+        prefetch_tensormap(tmK);
+        prefetch_tensormap(tmV);
+    }
+    uint32_t g0 = 0;  // key tiles of the pieces before
+    bool ok = true;
+    for (int piece = 0; ok && w.next(p); ++piece) {
+        const int32_t *bt = p.tables + (long long)w.b * p.max_blocks;
+        const int n_keys = w.len.ctx + w.len.drafts;
+        // page of this lane's chunk, read one tile ahead
+        auto page_of = [&](int tile) -> int {
+            const long long j = (long long)tile * TK + lane * p.box_rows;
+            return lane * p.box_rows < TK && j < n_keys ? bt[j >> p.shift] : -1;
+        };
+        const int n = w.t_b - w.t_a;
+        int page = page_of(w.t_a);
+        for (int g = 0; ok && g < n; ++g) {
+            const int tile = w.t_a + g;
+            const uint32_t G = g0 + g;
+            const int j = tile * TK + lane * p.box_rows;
+            const bool mine = lane * p.box_rows < TK && j < n_keys;
+            const int n_chunks = (min(TK, n_keys - tile * TK) + p.box_rows - 1) / p.box_rows;
+            // a page outside the pool reads as zeros (a group past the tensor map)
+            int group = p.num_blocks << (p.shift - 3);
+            if (mine) {
+                if (page >= 0 && page < p.num_blocks)
+                    group = (page << (p.shift - 3)) + ((j & ((1 << p.shift) - 1)) >> 3);
+                else
+                    record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+            }
+            if (g + 1 < n) page = page_of(tile + 1);
+            const uint32_t st = is_v ? C::NK + G % C::NV : G % C::NK, use = is_v ? G / C::NV : G / C::NK;
+            if (use > 0)
+                ok = warp_wait(bar(C::BAR_EMPTY + st), (use - 1) & 1, abort_flag, p.wait_limit_ns, p.status);
+            // checked build: the chunks stay inside the slot and the head inside the pool
+            ok = ok && in_range(n_chunks * p.box_rows <= TK && w.hkv < p.Hkv && w.b < p.B &&
+                                    tile >= w.t_a && tile < w.t_b,
+                                p.status, abort_flag);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::BAR_FULL + st), n_chunks * p.box_rows * D * 2);
+            __syncwarp();
+            if (mine)
+                tma_load_5d(sbase + C::OFF_RING + st * C::TILE + lane * (p.box_rows >> 3) * C::GROUP,
+                            is_v ? tmV : tmK, bar(C::BAR_FULL + st), 0, 0, 0, group, w.hkv);
+            // Q after the piece's first K, which need not wait for its slot
+            if (g == 0 && !is_v && lane == 0) {
+                if (piece > 0 && !mbar_wait(bar(C::BAR_QFREE), (piece - 1) & 1, abort_flag, p.wait_limit_ns,
+                                            p.status)) {
+                    ok = false;
+                } else {
+                    const int row0 = (w.b * p.Hq + w.hkv * (p.Hq / p.Hkv)) * p.T + w.rt * C::ROWS;
+                    const int n_q = C::NQ == 2 && tree_rows<C>(p, w.rt, 1) > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(bar(C::BAR_QFULL), n_q * C::QTILE);
+                    for (int t = 0; t < n_q; ++t)
+                        for (int c = 0; c < C::NBOX; ++c)
+                            tma_load_3d(sbase + C::OFF_Q + t * C::QTILE + c * C::QBOX, tmQ,
+                                        bar(C::BAR_QFULL), c * 64, row0 + t * C::RQ, 0);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        g0 += n;
+    }
+}
+
 template <int D, bool kTwo>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -191,152 +350,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8 * i; };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
-    int *first_b = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);
-    long long *first_pre = reinterpret_cast<long long *>(smem + C::OFF_ML);  // before the first piece
-    long long *warp_sums = first_pre + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::N_BARS; ++i)
-            mbar_init(bar(i), i == C::BAR_P || i == C::BAR_P + 1 ? TM : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // This CTA's run of the list, and the sequence it begins in.
     TreeWalk w;
-    {
-        const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
-        const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-        long long mine = 0, total;
-        for (int b = b0; b < b1; ++b) mine += tree_lens(p, b, blockIdx.x == 0).nt;
-        const long long before = block_scan(mine, warp_sums, total);
-        const long long H = (long long)p.Hkv * p.n_rt;
-        const long long share = (total * H + p.n_cta - 1) / p.n_cta;
-        w.f_first = w.f = blockIdx.x * share;
-        w.f_end = min(total * H, w.f + share);
-        if (w.f >= w.f_end) return;
-        if (before * H <= w.f && w.f < (before + mine) * H) {
-            long long pre = before;
-            int b = b0;
-            for (;; ++b) {
-                const int nt = tree_lens(p, b, false).nt;
-                if (w.f < (pre + nt) * H) break;
-                pre += nt;
-            }
-            *first_b = b;
-            *first_pre = pre;
-        }
-    }
-    if (warp == kWarpMma) {
-        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    w.b = *first_b;
-    w.pre = *first_pre;
-    w.len = tree_lens(p, w.b, false);
-    __syncthreads();  // the exchange area is reused from here on
-
-    auto slot_addr = [&](uint32_t e) -> uint32_t { return sbase + C::OFF_RING + (e % C::NS) * C::TILE; };
-    // rows of tile t of the segment that exist
-    auto rows_of = [&](int rt, int t) -> int { return min(TM, p.R - (rt * C::NQ + t) * TM); };
+    uint32_t tmem;
+    if (!tree_setup<C>(p, smem, w, tmem)) return;
+    auto slot_addr = [&](uint32_t st) -> uint32_t { return sbase + C::OFF_RING + st * C::TILE; };
+    auto rows_of = [&](int rt, int t) -> int { return tree_rows<C>(p, rt, t); };
 
     if (warp >= kWarpLoad) regs_dec<kLoadRegs>();
-    if (warp == kWarpLoad) {
-        // ===================== TMA producer =====================
-        if (lane == 0) {
-            prefetch_tensormap(&tmQ);
-            prefetch_tensormap(&tmK);
-            prefetch_tensormap(&tmV);
-        }
-        uint32_t e = 0;
-        bool ok = true;
-        for (int piece = 0; ok && w.next(p); ++piece) {
-            const int32_t *bt = p.tables + (long long)w.b * p.max_blocks;
-            const int n_keys = w.len.ctx + w.len.drafts;
-            // page of this lane's chunk, read one tile ahead
-            auto page_of = [&](int tile) -> int {
-                const long long j = (long long)tile * TK + lane * p.box_rows;
-                return lane * p.box_rows < TK && j < n_keys ? bt[j >> p.shift] : -1;
-            };
-            int page = page_of(w.t_a);
-            for (int tile = w.t_a; ok && tile < w.t_b; ++tile) {
-                const int j = tile * TK + lane * p.box_rows;
-                const bool mine = lane * p.box_rows < TK && j < n_keys;
-                const int n_chunks = (min(TK, n_keys - tile * TK) + p.box_rows - 1) / p.box_rows;
-                // a page outside the pool reads as zeros (a group past the tensor map)
-                int group = p.num_blocks << (p.shift - 3);
-                if (mine) {
-                    if (page >= 0 && page < p.num_blocks)
-                        group = (page << (p.shift - 3)) + ((j & ((1 << p.shift) - 1)) >> 3);
-                    else
-                        record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-                }
-                if (tile + 1 < w.t_b) page = page_of(tile + 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t st = e % C::NS, use = e / C::NS;
-                    if (ok && use > 0)
-                        ok = warp_wait(bar(C::BAR_EMPTY + st), (use - 1) & 1, abort_flag,
-                                       p.wait_limit_ns, p.status);
-                    // checked build: the chunks stay inside the slot and the head inside the pool
-                    ok = ok && in_range(n_chunks * p.box_rows <= TK && w.hkv < p.Hkv && w.b < p.B,
-                                        p.status, abort_flag);
-                    if (!ok) break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(bar(C::BAR_FULL + st), n_chunks * p.box_rows * D * 2);
-                    __syncwarp();
-                    if (mine)
-                        tma_load_5d(slot_addr(e) + lane * (p.box_rows >> 3) * C::GROUP, kv ? &tmV : &tmK,
-                                    bar(C::BAR_FULL + st), 0, 0, 0, group, w.hkv);
-                    ++e;
-                }
-                // Q after the piece's first K and V, which need not wait for its slot
-                if (ok && tile == w.t_a && lane == 0) {
-                    if (piece > 0 && !mbar_wait(bar(C::BAR_QFREE), (piece - 1) & 1, abort_flag,
-                                                p.wait_limit_ns, p.status)) {
-                        ok = false;
-                    } else {
-                        const int row0 = (w.b * p.Hq + w.hkv * (p.Hq / p.Hkv)) * p.T + w.rt * C::ROWS;
-                        const bool two = kTwo && rows_of(w.rt, 1) > 0;
-                        mbar_arrive_expect_tx(bar(C::BAR_QFULL), (two ? 2 : 1) * C::TILE);
-                        for (int t = 0; t < (two ? 2 : 1); ++t)
-                            for (int c = 0; c < C::NBOX; ++c)
-                                tma_load_3d(sbase + C::OFF_Q + t * C::TILE + c * C::QBOX, &tmQ,
-                                            bar(C::BAR_QFULL), c * 64, row0 + t * TM, 0);
-                    }
-                }
-                ok = __all_sync(0xffffffffu, ok);
-            }
-        }
+    if (warp == kWarpLoad || warp == kWarpLoadV) {
+        tree_produce<D, C>(p, smem, w, warp == kWarpLoadV, &tmQ, &tmK, &tmV);
     } else if (warp == kWarpMma) {
         // ===================== MMA issuer =====================
         if (lane == 0) {
             constexpr uint32_t idS = idesc_bf16_f32(TM, TK, 0, 0);
             constexpr uint32_t idO = idesc_bf16_f32(TM, D, 0, 1);
-            uint32_t e0 = 0, np0 = 0, np1 = 0;
+            uint32_t g0 = 0, np0 = 0, np1 = 0;
             bool ok = true;
             for (int piece = 0; ok && w.next(p); ++piece) {
                 const int n = w.t_b - w.t_a;
                 const bool two = kTwo && rows_of(w.rt, 1) > 0;
-                auto full = [&](uint32_t e) -> bool {
-                    return mbar_wait(bar(C::BAR_FULL + e % C::NS), (e / C::NS) & 1, abort_flag,
-                                     p.wait_limit_ns, p.status);
+                auto full = [&](uint32_t st, uint32_t use) -> bool {
+                    return mbar_wait(bar(C::BAR_FULL + st), use & 1, abort_flag, p.wait_limit_ns, p.status);
                 };
                 // S = Q K^T of key tile g into buffer t, from row tile q
                 auto issue_s = [&](int g, int t, int q, bool last_use) -> bool {
-                    const uint32_t e = e0 + 2 * g;
-                    if (!full(e)) return false;
+                    const uint32_t st = (g0 + g) % C::NK;
+                    if (!full(st, (g0 + g) / C::NK)) return false;
                     tc_fence_after();
-                    const uint32_t qa = sbase + C::OFF_Q + q * C::TILE, ka = slot_addr(e);
+                    const uint32_t qa = sbase + C::OFF_Q + q * C::TILE, ka = slot_addr(st);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         mma_ss(tmem + C::s_col(t),
@@ -344,26 +387,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                smem_desc_sw128(ka + (kk >> 2) * 1024 + (kk & 3) * 32, 16, C::GROUP), idS,
                                kk > 0 ? 1u : 0u);
                     mma_commit(bar(C::BAR_S + t));
-                    if (last_use) mma_commit(bar(C::BAR_EMPTY + e % C::NS));
+                    if (last_use) mma_commit(bar(C::BAR_EMPTY + st));
                     if (last_use && g == n - 1) mma_commit(bar(C::BAR_QFREE));
                     return true;
                 };
                 // O_t += P_t V of key tile g; `first` opens the accumulator, `last` closes it
                 auto issue_pv = [&](int g, int t, bool first, bool last, bool last_use) -> bool {
-                    const uint32_t e = e0 + 2 * g + 1;
+                    const uint32_t st = C::NK + (g0 + g) % C::NV;
                     const uint32_t np = t ? np1++ : np0++;
                     if (!mbar_wait(bar(C::BAR_P + t), np & 1, abort_flag, p.wait_limit_ns, p.status) ||
-                        !full(e))
+                        !full(st, (g0 + g) / C::NV))
                         return false;
                     tc_fence_after();
-                    const uint32_t va = slot_addr(e);
+                    const uint32_t va = slot_addr(st);
 #pragma unroll
                     for (int kk = 0; kk < TK / 16; ++kk)
                         mma_ts(tmem + C::o_col(t), tmem + C::s_col(t) + kk * 8,
                                smem_desc_sw128(va + kk * 2 * C::GROUP, 1024, C::GROUP), idO,
                                !first || kk > 0 ? 1u : 0u);
                     if (last) mma_commit(bar(C::BAR_O + t));
-                    if (last_use) mma_commit(bar(C::BAR_EMPTY + e % C::NS));
+                    if (last_use) mma_commit(bar(C::BAR_EMPTY + st));
                     return true;
                 };
                 ok = mbar_wait(bar(C::BAR_QFULL), piece & 1, abort_flag, p.wait_limit_ns, p.status);
@@ -383,7 +426,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                  (last || issue_s(g + 1, 1, 1, true));
                     }
                 }
-                e0 += 2 * n;
+                g0 += n;
             }
         }
     } else if (warp < kWarpLoad) {
@@ -395,7 +438,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t o_addr = trow + (t ? C::o_col(1) : C::o_col(0));
         float *ml = reinterpret_cast<float *>(smem + C::OFF_ML);
         uint8_t *par = smem + C::OFF_PAR + t * kMaxDrafts;
-        uint32_t n_s = 0, n_o = 0, e0 = 0;  // S tiles, accumulators and ring entries so far
+        uint32_t n_s = 0, n_o = 0, g0 = 0;  // S tiles, accumulators and key tiles so far
         bool ok = true;
         while (ok && w.next(p)) {
             const int ctx = w.len.ctx, n_keys = ctx + w.len.drafts;
@@ -430,14 +473,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 // V rows past the keys may hold anything; their weights are 0, but 0 * NaN is
                 // NaN, so this tile's (first) warpgroup zeroes them
                 if (kv0 + TK > n_keys && (!kTwo || t == 0)) {
-                    const uint32_t e = e0 + 2 * g + 1;
-                    if (!warp_wait(bar(C::BAR_FULL + e % C::NS), (e / C::NS) & 1, abort_flag,
+                    const uint32_t st = C::NK + (g0 + g) % C::NV;
+                    if (!warp_wait(bar(C::BAR_FULL + st), ((g0 + g) / C::NV) & 1, abort_flag,
                                    p.wait_limit_ns, p.status)) {
                         ok = false;
                         break;
                     }
                     if (kv0 + r >= n_keys) {
-                        uint8_t *v = smem + C::OFF_RING + (e % C::NS) * C::TILE + (r >> 3) * C::GROUP +
+                        uint8_t *v = smem + C::OFF_RING + st * C::TILE + (r >> 3) * C::GROUP +
                                      (r & 7) * 128;
 #pragma unroll
                         for (int c = 0; c < C::NBOX; ++c)
@@ -538,7 +581,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 ++n_o;
             }
             n_s += n_iter;
-            e0 += 2 * n;
+            g0 += n;
             float a0 = 1.f, a1 = 0.f, m = m_used;  // factors of O_0 and O_1 for this row
             int c_lo = 0, c_hi = D / 32;            // 32-column chunks this warpgroup writes
             const bool whole = w.whole();
@@ -634,15 +677,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             ok = all_of_256(ok);
         }
     }
-    // ---- teardown ----
-    if (*abort_flag) drain_delay(2000000);  // let copies and MMAs in flight land
-    tc_fence_before();
-    __syncthreads();
-    if (warp == kWarpMma) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
-    }
+    tree_teardown<C>(smem, tmem);
 }
 
 // Rows of the segments that several CTAs worked on, from their partial states; rows of
@@ -652,10 +687,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // a piece's max before its row).
 constexpr int kCombineThreads = 256;
 
-template <int D, bool kTwo>
+template <int D, class C>
 __global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const TreeParams p, int row_blocks, int rows_per_block) {
-    using C = TreeCfg<D, kTwo>;
     constexpr int PER = D / 32;
     __shared__ long long warp_sums[kCombineThreads / 32], found;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -734,9 +768,9 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
 }
 
-template <int D, bool kTwo>
-attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream) {
-    using C = TreeCfg<D, kTwo>;
+template <int D, class C>
+attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
+                            void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, TreeParams)) {
     TreeParams p;
     p.O = static_cast<__nv_bfloat16 *>(a.O);
     p.tables = a.block_tables;
@@ -765,12 +799,11 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     attn_status_t st;
     const uint64_t rows = (uint64_t)a.num_blocks * a.block_size;
-    if ((st = make_tmap_bf16_3d(&tq, a.Q, D, (uint64_t)a.B * a.Hq * a.T, 1, TM)) != ATTN_OK ||
+    if ((st = make_tmap_bf16_3d(&tq, a.Q, D, (uint64_t)a.B * a.Hq * a.T, 1, C::RQ)) != ATTN_OK ||
         (st = make_tmap_bf16_paged_groups(&tk, a.K, D, a.Hkv, rows, p.box_rows)) != ATTN_OK ||
         (st = make_tmap_bf16_paged_groups(&tv, a.V, D, a.Hkv, rows, p.box_rows)) != ATTN_OK)
         return st;
-    if (kernel_setup(reinterpret_cast<const void *>(tree_kernel<D, kTwo>), C::SMEM, kTreeRegs) !=
-        cudaSuccess)
+    if (kernel_setup(reinterpret_cast<const void *>(kernel), C::SMEM, kTreeRegs) != cudaSuccess)
         return ATTN_ERR_CUDA;
     void *ws = nullptr;
     if (workspace_alloc(&ws, (size_t)2 * p.n_cta * C::WS * sizeof(float), stream) != cudaSuccess)
@@ -786,8 +819,7 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    st = cudaLaunchKernelEx(&cfg, tree_kernel<D, kTwo>, tq, tk, tv, p) == cudaSuccess ? ATTN_OK
-                                                                                     : ATTN_ERR_CUDA;
+    st = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     // a row per warp while the blocks fit on the SMs at once, four where that leaves more
     // blocks that only find their segment whole
     const long long fine = ((long long)p.R + 7) / 8 * a.B * a.Hkv;
@@ -797,7 +829,7 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream) {
         cfg.gridDim = dim3(static_cast<unsigned>(row_blocks) * a.B * a.Hkv, 1, 1);
         cfg.blockDim = dim3(kCombineThreads, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, kTwo>, p, row_blocks, rows_per_block) != cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, C>, p, row_blocks, rows_per_block) != cudaSuccess)
             st = ATTN_ERR_CUDA;
     }
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
@@ -811,8 +843,15 @@ attn_status_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
     if ((long long)a.B * a.Hq * a.T > 0x7fffffffll - 2 * TM ||
         (long long)a.B * a.Hkv * ((R + 31) / 32) > 0x7fffffffll)
         return ATTN_ERR_INVALID;
-    if (a.D == 128) return R > TM ? launch_tree_d<128, true>(a, stream) : launch_tree_d<128, false>(a, stream);
-    return R > TM ? launch_tree_d<64, true>(a, stream) : launch_tree_d<64, false>(a, stream);
+#define GQA_LAUNCH(DD)                                                                              \
+    do {                                                                                            \
+        if (R <= TM)                                                                                \
+            return launch_tree_d<DD, TreeCfg<DD, false>>(a, stream, tree_kernel<DD, false>);        \
+        return launch_tree_d<DD, TreeCfg<DD, true>>(a, stream, tree_kernel<DD, true>);              \
+    } while (0)
+    if (a.D == 128) GQA_LAUNCH(128);
+    GQA_LAUNCH(64);
+#undef GQA_LAUNCH
 }
 
 }  // namespace gqa
