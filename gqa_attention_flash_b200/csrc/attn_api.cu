@@ -405,8 +405,9 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
     if ((long long)B * Hkv > 0x7fffffffll) return ATTN_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t bytes = decode_workspace_floats(B, Hq, n_splits, D) * sizeof(float);
+    const bool needs_ws = window == 0 || !decode_sinks_in_cluster(n_splits);
     void *ws = nullptr;
-    if (workspace_alloc(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (needs_ws && workspace_alloc(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
     DecodeArgs a;
     a.O = O;
     a.Q = Q;
@@ -423,18 +424,21 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
     a.window = window;
     a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
-    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (needs_ws && cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return st;
 }
 
 // Slices per (sequence, KV head) when the caller leaves them to the library: enough for
-// two blocks per SM, and at most one per 64-key tile that can hold a visible key.
+// two blocks per SM, and at most one per 64-key tile that can hold a visible key.  Up to 8
+// slices need no workspace and no second kernel, so more are made only where 8 would be
+// left with more than 32 tiles each.
 int sink_splits(int B, int Hkv, long long S_cap, int window, int sinks) {
     const long long tiles = std::min((std::min<long long>(window, S_cap) + 62) / 64 + 1 +
                                          (std::min<long long>(sinks, S_cap) + 63) / 64,
                                      (S_cap + 63) / 64);
     const long long pairs = std::max(1ll, (long long)B * Hkv);
-    return static_cast<int>(std::max(1ll, std::min({(2 * 148 + pairs - 1) / pairs, tiles, 64ll})));
+    const long long n = std::max(1ll, std::min({(2 * 148 + pairs - 1) / pairs, tiles, 64ll}));
+    return static_cast<int>(n > 8 && tiles <= 8 * 32 ? 8 : n);
 }
 
 }  // namespace
@@ -608,8 +612,9 @@ attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const vo
         return ATTN_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t bytes = decode_workspace_floats(B, Hq, n_splits, D) * sizeof(float);
+    const bool needs_ws = window == 0 || !decode_sinks_in_cluster(n_splits);
     void *ws = nullptr;
-    if (workspace_alloc(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (needs_ws && workspace_alloc(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
     DecodeArgs a;
     a.O = O;
     a.Q = Q;
@@ -630,7 +635,7 @@ attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const vo
     a.window = window;
     a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
-    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (needs_ws && cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return st;
 }
 

@@ -31,6 +31,9 @@
 // The slices then divide the 64-key tiles that hold such a key; chunks of a paged tile
 // without one are not read (their pages may have been freed), and the V rows of keys
 // that are not visible are zeroed in shared memory before they meet their zero weights.
+// A window is short, so its decode is a matter of latency: up to 8 slices run as one
+// thread-block cluster that merges its partials through distributed shared memory, with
+// no workspace and no second kernel (B1, window 1024: 9.7 -> 7.6 us a call back to back).
 //
 // Kernel 2 (combine): one warp per (sequence, query head) merges the slices:
 // LSE = log sum_s exp(lse_s), O = sum_s exp(lse_s - LSE) o_s; empty slices
@@ -63,12 +66,16 @@ struct DecCfg {
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
     // merge area (reuses the ring once every tile is consumed)
     static constexpr int MERGE_BYTES = kConsumers * kMaxGroup * (D + 2) * 4;
-    static_assert(MERGE_BYTES <= 2 * NS * TILE, "merge area must fit in the ring");
+    static_assert(MERGE_BYTES + kMaxGroup * (D + 1) * 4 <= 2 * NS * TILE,
+                  "merge area and a slice's partials must fit in the ring");
     static constexpr int WS_STRIDE = D + 4;     // floats per partial: o[D], lse, pad
 };
 
+constexpr int kMaxCluster = 8;  // slices of one cluster (the portable cluster size)
+
 struct DecParams {
     const __nv_bfloat16 *Q;
+    __nv_bfloat16 *O;  // kCluster only
     float *ws;
     const int32_t *lengths;
     int B, Hq, Hkv, S_cap, group, n_splits;
@@ -128,7 +135,23 @@ __device__ __forceinline__ uint32_t swz_t(int row, int chunk) {
     }
 }
 
-template <int D, bool kPaged, bool kSink>
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// fp32 at this CTA's shared-memory address `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+    uint32_t a;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// kCluster: the grid's x dimension is one cluster per (KV head, sequence); the partials
+// stay in shared memory and each CTA merges its share of the G D outputs of all slices.
+template <int D, bool kPaged, bool kSink, bool kCluster>
 __global__ void __launch_bounds__(kDecThreads)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const DecParams p) {
@@ -168,299 +191,342 @@ __global__ void __launch_bounds__(kDecThreads)
     const int k0 = split * per * TN;
     const int k1 = kSink ? min(k0 + per * TN, n_all * TN) : min(k0 + per * TN, len);
 
+    // kCluster: this slice's partials, [G][D] outputs and [G] log-sum-exps, behind the
+    // four warps' merge area
+    float *part = reinterpret_cast<float *>(smem + C::MERGE_BYTES);
+
     float *ws_base = p.ws + ((long long)(b * p.Hq + h0) * p.n_splits + split) * C::WS_STRIDE;
     const long long ws_head = (long long)p.n_splits * C::WS_STRIDE;
     // checked build: the workspace entries of this CTA's G heads lie inside it
     const long long ws_end = (long long)p.B * p.Hq * p.n_splits * C::WS_STRIDE;
-    const bool ws_ok = in_range(
+    const bool ws_ok = kCluster || in_range(
         ((long long)(b * p.Hq + h0 + G - 1) * p.n_splits + split) * C::WS_STRIDE + D < ws_end,
         p.status, nullptr);
 
     if (k0 >= k1) {  // empty slice: weight zero in the combine
-        for (int h = threadIdx.x; h < G && ws_ok; h += blockDim.x) ws_base[h * ws_head + D] = neg_inf();
-        return;
-    }
-    const int t_begin = k0 / TN;
-    const int n_tiles = (k1 + TN - 1) / TN - t_begin;
-    // first key of the slice's tile `it`
-    auto tile_row = [&](int it) -> int { return (kSink ? vis.tile(t_begin + it) : t_begin + it) * TN; };
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), kConsumers);
+        if constexpr (!kCluster) {
+            for (int h = threadIdx.x; h < G && ws_ok; h += blockDim.x) ws_base[h * ws_head + D] = neg_inf();
+            return;
+        } else {
+            for (int h = threadIdx.x; h < G; h += blockDim.x) part[G * D + h] = neg_inf();
+            if (threadIdx.x == 0) *abort_flag = 0;
+            __syncthreads();
         }
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    __syncthreads();
+    } else {
+        const int t_begin = k0 / TN;
+        const int n_tiles = (k1 + TN - 1) / TN - t_begin;
+        // first key of the slice's tile `it`
+        auto tile_row = [&](int it) -> int { return (kSink ? vis.tile(t_begin + it) : t_begin + it) * TN; };
 
-    if (warp == kConsumers) {
-        // ===================== TMA producer =====================
-        if (lane == 0) {
-            prefetch_tensormap(&tmK);
-            prefetch_tensormap(&tmV);
-            // paged: block ids of a tile's chunks, loaded one tile ahead so that the
-            // block-table reads overlap the previous tile's copies instead of each
-            // copy waiting for its own read (block_size >= 8: at most TN / 8 chunks)
-            constexpr int kMaxChunks = TN / 8;
-            int ids[kMaxChunks];
-            auto load_ids = [&](int it2) {
-                if constexpr (kPaged) {
-                    const int row2 = tile_row(it2);
-                    const int n2 = (min(TN, len - row2) + p.box_rows - 1) / p.box_rows;
-                    const int32_t *bt = p.block_tables + (long long)b * p.max_blocks;
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < C::NS; ++s) {
+                mbar_init(full(s), 1);
+                mbar_init(empty(s), kConsumers);
+            }
+            *abort_flag = 0;
+            fence_mbar_init();
+        }
+        __syncthreads();
+
+        if (warp == kConsumers) {
+            // ===================== TMA producer =====================
+            if (lane == 0) {
+                prefetch_tensormap(&tmK);
+                prefetch_tensormap(&tmV);
+                // paged: block ids of a tile's chunks, loaded one tile ahead so that the
+                // block-table reads overlap the previous tile's copies instead of each
+                // copy waiting for its own read (block_size >= 8: at most TN / 8 chunks)
+                constexpr int kMaxChunks = TN / 8;
+                int ids[kMaxChunks];
+                auto load_ids = [&](int it2) {
+                    if constexpr (kPaged) {
+                        const int row2 = tile_row(it2);
+                        const int n2 = (min(TN, len - row2) + p.box_rows - 1) / p.box_rows;
+                        const int32_t *bt = p.block_tables + (long long)b * p.max_blocks;
 #pragma unroll
-                    for (int k = 0; k < kMaxChunks; ++k)
-                        ids[k] = k < n2 ? bt[(row2 + k * p.box_rows) >> p.block_shift] : 0;
-                }
-            };
-            if (n_tiles > 0) load_ids(0);
-            for (int it = 0; it < n_tiles; ++it) {
-                const int st = it % C::NS;
-                const int use = it / C::NS;
-                if (use > 0 &&
-                    !mbar_wait(empty(st), (use - 1) & 1, abort_flag, p.wait_limit_ns, p.status))
-                    break;
-                const int row = tile_row(it);
-                if constexpr (!kPaged) {
-                    if (!in_range(box_ok(0, row, b * p.Hkv + hkv, D, p.S_cap, (long long)p.B * p.Hkv,
-                                         TN) &&
-                                      row >= 0 && row < p.S_cap,
-                                  p.status, abort_flag))
+                        for (int k = 0; k < kMaxChunks; ++k)
+                            ids[k] = k < n2 ? bt[(row2 + k * p.box_rows) >> p.block_shift] : 0;
+                    }
+                };
+                if (n_tiles > 0) load_ids(0);
+                for (int it = 0; it < n_tiles; ++it) {
+                    const int st = it % C::NS;
+                    const int use = it / C::NS;
+                    if (use > 0 &&
+                        !mbar_wait(empty(st), (use - 1) & 1, abort_flag, p.wait_limit_ns, p.status))
                         break;
-                    mbar_arrive_expect_tx(full(st), 2 * C::TILE);
-                    for (int c = 0; c < C::NBOX; ++c) {
-                        tma_load_3d(sbase + C::OFF_K + st * C::TILE + c * C::BOX, &tmK, full(st),
-                                    c * 64, row, b * p.Hkv + hkv);
-                        tma_load_3d(sbase + C::OFF_V + st * C::TILE + c * C::BOX, &tmV, full(st),
-                                    c * 64, row, b * p.Hkv + hkv);
-                    }
-                } else {
-                    // Gather the tile's valid keys chunk by chunk: key j of the sequence
-                    // is cache row block_tables[b][j / block_size] * block_size +
-                    // j % block_size.  Chunks past the length are not loaded; the
-                    // consumers mask those keys and zero those V rows.
-                    const int br = p.box_rows;
-                    const int n_chunks = (min(TN, len - row) + br - 1) / br;
-                    int cur[kMaxChunks];
+                    const int row = tile_row(it);
+                    if constexpr (!kPaged) {
+                        if (!in_range(box_ok(0, row, b * p.Hkv + hkv, D, p.S_cap, (long long)p.B * p.Hkv,
+                                             TN) &&
+                                          row >= 0 && row < p.S_cap,
+                                      p.status, abort_flag))
+                            break;
+                        mbar_arrive_expect_tx(full(st), 2 * C::TILE);
+                        for (int c = 0; c < C::NBOX; ++c) {
+                            tma_load_3d(sbase + C::OFF_K + st * C::TILE + c * C::BOX, &tmK, full(st),
+                                        c * 64, row, b * p.Hkv + hkv);
+                            tma_load_3d(sbase + C::OFF_V + st * C::TILE + c * C::BOX, &tmV, full(st),
+                                        c * 64, row, b * p.Hkv + hkv);
+                        }
+                    } else {
+                        // Gather the tile's valid keys chunk by chunk: key j of the sequence
+                        // is cache row block_tables[b][j / block_size] * block_size +
+                        // j % block_size.  Chunks past the length are not loaded; the
+                        // consumers mask those keys and zero those V rows.
+                        const int br = p.box_rows;
+                        const int n_chunks = (min(TN, len - row) + br - 1) / br;
+                        int cur[kMaxChunks];
 #pragma unroll
-                    for (int k = 0; k < kMaxChunks; ++k) cur[k] = ids[k];
-                    if (it + 1 < n_tiles) load_ids(it + 1);
-                    int n_read = n_chunks;
-                    if constexpr (kSink) {
-                        n_read = 0;
-                        for (int k = 0; k < n_chunks; ++k) n_read += vis.any(row + k * br, br) ? 1 : 0;
-                    }
-                    mbar_arrive_expect_tx(full(st), 2 * n_read * br * 128 * C::NBOX);
+                        for (int k = 0; k < kMaxChunks; ++k) cur[k] = ids[k];
+                        if (it + 1 < n_tiles) load_ids(it + 1);
+                        int n_read = n_chunks;
+                        if constexpr (kSink) {
+                            n_read = 0;
+                            for (int k = 0; k < n_chunks; ++k) n_read += vis.any(row + k * br, br) ? 1 : 0;
+                        }
+                        mbar_arrive_expect_tx(full(st), 2 * n_read * br * 128 * C::NBOX);
 #pragma unroll
-                    for (int k = 0; k < kMaxChunks; ++k) {
-                        if (k >= n_chunks) break;
-                        const int j = row + k * br;
-                        if (kSink && !vis.any(j, br)) continue;
-                        const int blk = cur[k];
-                        if (blk < 0 || blk >= p.num_blocks) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-                        // an out-of-range block reads as zeros (outside the tensor map)
-                        const int prow = blk * (1 << p.block_shift) + (j & ((1 << p.block_shift) - 1));
-                        // checked build: the chunk stays inside its tile of the ring (an
-                        // out-of-range block is the documented zero-filled case)
-                        if (!in_range(k * br + br <= TN && hkv < p.Hkv, p.status, abort_flag)) break;
-                        if constexpr (kWide) {
-                            const uint32_t off = st * C::TILE + k * br * 256;
-                            tma_load_4d(sbase + C::OFF_K + off, &tmK, full(st), 0, 0, hkv, prow);
-                            tma_load_4d(sbase + C::OFF_V + off, &tmV, full(st), 0, 0, hkv, prow);
-                        } else {
-                            for (int c = 0; c < C::NBOX; ++c) {
-                                const uint32_t off = st * C::TILE + c * C::BOX + k * br * 128;
-                                tma_load_3d(sbase + C::OFF_K + off, &tmK, full(st), c * 64, hkv, prow);
-                                tma_load_3d(sbase + C::OFF_V + off, &tmV, full(st), c * 64, hkv, prow);
+                        for (int k = 0; k < kMaxChunks; ++k) {
+                            if (k >= n_chunks) break;
+                            const int j = row + k * br;
+                            if (kSink && !vis.any(j, br)) continue;
+                            const int blk = cur[k];
+                            if (blk < 0 || blk >= p.num_blocks) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+                            // an out-of-range block reads as zeros (outside the tensor map)
+                            const int prow = blk * (1 << p.block_shift) + (j & ((1 << p.block_shift) - 1));
+                            // checked build: the chunk stays inside its tile of the ring (an
+                            // out-of-range block is the documented zero-filled case)
+                            if (!in_range(k * br + br <= TN && hkv < p.Hkv, p.status, abort_flag)) break;
+                            if constexpr (kWide) {
+                                const uint32_t off = st * C::TILE + k * br * 256;
+                                tma_load_4d(sbase + C::OFF_K + off, &tmK, full(st), 0, 0, hkv, prow);
+                                tma_load_4d(sbase + C::OFF_V + off, &tmV, full(st), 0, 0, hkv, prow);
+                            } else {
+                                for (int c = 0; c < C::NBOX; ++c) {
+                                    const uint32_t off = st * C::TILE + c * C::BOX + k * br * 128;
+                                    tma_load_3d(sbase + C::OFF_K + off, &tmK, full(st), c * 64, hkv, prow);
+                                    tma_load_3d(sbase + C::OFF_V + off, &tmV, full(st), c * 64, hkv, prow);
+                                }
                             }
                         }
                     }
                 }
             }
-        }
-    } else {
-        // ===================== consumers =====================
-        const int g = lane >> 2;  // fragment row (query head within the group)
-        const int t = lane & 3;
-        // Q as m16n8k16 A fragments: rows = query heads (zero past G), k = d.
-        uint32_t qa[D / 16][4];
-        {
-            const __nv_bfloat16 *q_lo = p.Q + (long long)(b * p.Hq + h0 + g) * D;
-            const __nv_bfloat16 *q_hi = p.Q + (long long)(b * p.Hq + h0 + g + 8) * D;
-            const bool lo_ok = g < G, hi_ok = g + 8 < G;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int c0 = kk * 16 + 2 * t;
-                qa[kk][0] = lo_ok ? *reinterpret_cast<const uint32_t *>(q_lo + c0) : 0u;
-                qa[kk][1] = hi_ok ? *reinterpret_cast<const uint32_t *>(q_hi + c0) : 0u;
-                qa[kk][2] = lo_ok ? *reinterpret_cast<const uint32_t *>(q_lo + c0 + 8) : 0u;
-                qa[kk][3] = hi_ok ? *reinterpret_cast<const uint32_t *>(q_hi + c0 + 8) : 0u;
-            }
-        }
-        float o[D / 8][4];
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        float m_run[2] = {neg_inf(), neg_inf()};  // rows g, g + 8 (log2 units)
-        float l_run[2] = {0.f, 0.f};              // this lane's partial row sums
-
-        // ldmatrix lane roles
-        const int mi = lane >> 3, rr = lane & 7;
-        bool ok = true;
-        for (int it = 0; it < n_tiles; ++it) {
-            const int st = it % C::NS;
-            if (!warp_wait(full(st), (it / C::NS) & 1, abort_flag, p.wait_limit_ns, p.status)) {
-                ok = false;
-                break;
-            }
-            const int key0 = tile_row(it) + warp * 16;  // first key of this warp
-            const int key_end = kSink ? len : k1;
-            if (key0 < key_end) {
-                const uint32_t kb = sbase + C::OFF_K + st * C::TILE;
-                const uint32_t vb = sbase + C::OFF_V + st * C::TILE;
-                // ---- S = Q K^T over this warp's 16 keys ----
-                float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                {
-                    const int krow = warp * 16 + (mi >> 1) * 8 + rr;
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        uint32_t b0, b1, b2, b3;
-                        ldmatrix_x4(kb + swz_t<kWide>(krow, 2 * kk + (mi & 1)), b0, b1, b2, b3);
-                        mma_m16n8k16(sc[0], qa[kk], b0, b1);
-                        mma_m16n8k16(sc[1], qa[kk], b2, b3);
-                    }
-                }
-                // ---- mask keys past the slice end; online softmax (exp2 domain) ----
-                float mt[2] = {neg_inf(), neg_inf()};
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + nb * 8 + 2 * t + (e & 1);
-                        const bool seen = key < key_end && (!kSink || vis.sees(key));
-                        const float x = seen ? sc[nb][e] * p.scale_log2 : neg_inf();
-                        sc[nb][e] = x;
-                        mt[e >> 1] = fmaxf(mt[e >> 1], x);
-                    }
-                float alpha[2], m_use[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
-                    mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
-                    const float m_new = fmaxf(m_run[h], mt[h]);
-                    m_use[h] = (m_new == neg_inf()) ? 0.f : m_new;
-                    alpha[h] = fast_exp2(m_run[h] - m_use[h]);
-                    m_run[h] = m_new;
-                }
-                float pr[2][4];
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) pr[nb][e] = fast_exp2(sc[nb][e] - m_use[e >> 1]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    l_run[h] = l_run[h] * alpha[h] + pr[0][2 * h] + pr[0][2 * h + 1] +
-                               pr[1][2 * h] + pr[1][2 * h + 1];
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[n][0] *= alpha[0];
-                    o[n][1] *= alpha[0];
-                    o[n][2] *= alpha[1];
-                    o[n][3] *= alpha[1];
-                }
-                uint32_t pa[4];
-                pa[0] = pack_bf16x2(pr[0][0], pr[0][1]);
-                pa[1] = pack_bf16x2(pr[0][2], pr[0][3]);
-                pa[2] = pack_bf16x2(pr[1][0], pr[1][1]);
-                pa[3] = pack_bf16x2(pr[1][2], pr[1][3]);
-                // Cache rows at or past the sequence length may hold anything; their
-                // weights are 0, but 0 * NaN is NaN, so zero this warp's such V rows.
-                // With a window, neither do the rows between the sinks and the window.
-                const bool cut = kSink && key0 < vis.win_lo && key0 + 16 > vis.sinks;
-                const bool tail = (key0 + 16 > len && key0 < p.S_cap) || cut;
-                if (tail) {
-                    const int rows_from = max(len - key0, 0);
-                    for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
-                        const int rrow = idx / (D / 8), ch = idx % (D / 8);
-                        if (rrow >= rows_from || (kSink && !vis.sees(key0 + rrow)))
-                            *reinterpret_cast<uint4 *>(smem + C::OFF_V + st * C::TILE +
-                                                       swz_t<kWide>(warp * 16 + rrow, ch)) =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                    __syncwarp();
-                }
-                // ---- O += P V over this warp's 16 keys ----
-                {
-                    const int vrow = warp * 16 + (mi & 1) * 8 + rr;
-#pragma unroll
-                    for (int dp = 0; dp < D / 16; ++dp) {
-                        uint32_t b0, b1, b2, b3;
-                        ldmatrix_x4_trans(vb + swz_t<kWide>(vrow, 2 * dp + (mi >> 1)), b0, b1, b2, b3);
-                        mma_m16n8k16(o[2 * dp], pa, b0, b1);
-                        mma_m16n8k16(o[2 * dp + 1], pa, b2, b3);
-                    }
-                }
-                if (tail) fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty(st));
-        }
-
-        // ---- merge the four warps' states (ring memory is free now) ----
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
-            l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
-        }
-        float *mrg = reinterpret_cast<float *>(smem);
-        // layout: [warp][row 0..15][D] outputs, then m[warp][16], l[warp][16]
-        float *mo = mrg;
-        float *mm = mrg + kConsumers * kMaxGroup * D;
-        float *ml = mm + kConsumers * kMaxGroup;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-            const int col = n * 8 + 2 * t;
-            mo[(warp * kMaxGroup + g) * D + col] = o[n][0];
-            mo[(warp * kMaxGroup + g) * D + col + 1] = o[n][1];
-            mo[(warp * kMaxGroup + g + 8) * D + col] = o[n][2];
-            mo[(warp * kMaxGroup + g + 8) * D + col + 1] = o[n][3];
-        }
-        if (t == 0) {
-            mm[warp * kMaxGroup + g] = m_run[0];
-            mm[warp * kMaxGroup + g + 8] = m_run[1];
-            ml[warp * kMaxGroup + g] = l_run[0];
-            ml[warp * kMaxGroup + g + 8] = l_run[1];
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
-        if (ok && !*abort_flag && ws_ok) {
-            for (int idx = threadIdx.x; idx < G * D; idx += 32 * kConsumers) {
-                const int h = idx / D, d = idx % D;
-                float M = neg_inf();
-#pragma unroll
-                for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, mm[w * kMaxGroup + h]);
-                float acc = 0.f, lsum = 0.f;
-#pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
-                    const float wt = fast_exp2(mm[w * kMaxGroup + h] - M);
-                    acc += wt * mo[(w * kMaxGroup + h) * D + d];
-                    lsum += wt * ml[w * kMaxGroup + h];
-                }
-                float *dst = ws_base + h * ws_head;
-                dst[d] = acc / lsum;
-                if (d == 0) dst[D] = (M + __log2f(lsum)) * 0.69314718055994531f;
-            }
         } else {
-            // A bounded wait ran out: the slice weighs nothing in the combine, so
-            // whatever the workspace held before (another call's partials) never
-            // reaches O.
-            for (int h = threadIdx.x; h < G && ws_ok; h += 32 * kConsumers)
-                ws_base[h * ws_head + D] = neg_inf();
+            // ===================== consumers =====================
+            const int g = lane >> 2;  // fragment row (query head within the group)
+            const int t = lane & 3;
+            // Q as m16n8k16 A fragments: rows = query heads (zero past G), k = d.
+            uint32_t qa[D / 16][4];
+            {
+                const __nv_bfloat16 *q_lo = p.Q + (long long)(b * p.Hq + h0 + g) * D;
+                const __nv_bfloat16 *q_hi = p.Q + (long long)(b * p.Hq + h0 + g + 8) * D;
+                const bool lo_ok = g < G, hi_ok = g + 8 < G;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int c0 = kk * 16 + 2 * t;
+                    qa[kk][0] = lo_ok ? *reinterpret_cast<const uint32_t *>(q_lo + c0) : 0u;
+                    qa[kk][1] = hi_ok ? *reinterpret_cast<const uint32_t *>(q_hi + c0) : 0u;
+                    qa[kk][2] = lo_ok ? *reinterpret_cast<const uint32_t *>(q_lo + c0 + 8) : 0u;
+                    qa[kk][3] = hi_ok ? *reinterpret_cast<const uint32_t *>(q_hi + c0 + 8) : 0u;
+                }
+            }
+            float o[D / 8][4];
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+            float m_run[2] = {neg_inf(), neg_inf()};  // rows g, g + 8 (log2 units)
+            float l_run[2] = {0.f, 0.f};              // this lane's partial row sums
+
+            // ldmatrix lane roles
+            const int mi = lane >> 3, rr = lane & 7;
+            bool ok = true;
+            for (int it = 0; it < n_tiles; ++it) {
+                const int st = it % C::NS;
+                if (!warp_wait(full(st), (it / C::NS) & 1, abort_flag, p.wait_limit_ns, p.status)) {
+                    ok = false;
+                    break;
+                }
+                const int key0 = tile_row(it) + warp * 16;  // first key of this warp
+                const int key_end = kSink ? len : k1;
+                if (key0 < key_end) {
+                    const uint32_t kb = sbase + C::OFF_K + st * C::TILE;
+                    const uint32_t vb = sbase + C::OFF_V + st * C::TILE;
+                    // ---- S = Q K^T over this warp's 16 keys ----
+                    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    {
+                        const int krow = warp * 16 + (mi >> 1) * 8 + rr;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            uint32_t b0, b1, b2, b3;
+                            ldmatrix_x4(kb + swz_t<kWide>(krow, 2 * kk + (mi & 1)), b0, b1, b2, b3);
+                            mma_m16n8k16(sc[0], qa[kk], b0, b1);
+                            mma_m16n8k16(sc[1], qa[kk], b2, b3);
+                        }
+                    }
+                    // ---- mask keys past the slice end; online softmax (exp2 domain) ----
+                    float mt[2] = {neg_inf(), neg_inf()};
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + nb * 8 + 2 * t + (e & 1);
+                            const bool seen = key < key_end && (!kSink || vis.sees(key));
+                            const float x = seen ? sc[nb][e] * p.scale_log2 : neg_inf();
+                            sc[nb][e] = x;
+                            mt[e >> 1] = fmaxf(mt[e >> 1], x);
+                        }
+                    float alpha[2], m_use[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 1));
+                        mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], 2));
+                        const float m_new = fmaxf(m_run[h], mt[h]);
+                        m_use[h] = (m_new == neg_inf()) ? 0.f : m_new;
+                        alpha[h] = fast_exp2(m_run[h] - m_use[h]);
+                        m_run[h] = m_new;
+                    }
+                    float pr[2][4];
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pr[nb][e] = fast_exp2(sc[nb][e] - m_use[e >> 1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        l_run[h] = l_run[h] * alpha[h] + pr[0][2 * h] + pr[0][2 * h + 1] +
+                                   pr[1][2 * h] + pr[1][2 * h + 1];
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        o[n][0] *= alpha[0];
+                        o[n][1] *= alpha[0];
+                        o[n][2] *= alpha[1];
+                        o[n][3] *= alpha[1];
+                    }
+                    uint32_t pa[4];
+                    pa[0] = pack_bf16x2(pr[0][0], pr[0][1]);
+                    pa[1] = pack_bf16x2(pr[0][2], pr[0][3]);
+                    pa[2] = pack_bf16x2(pr[1][0], pr[1][1]);
+                    pa[3] = pack_bf16x2(pr[1][2], pr[1][3]);
+                    // Cache rows at or past the sequence length may hold anything; their
+                    // weights are 0, but 0 * NaN is NaN, so zero this warp's such V rows.
+                    // With a window, neither do the rows between the sinks and the window.
+                    const bool cut = kSink && key0 < vis.win_lo && key0 + 16 > vis.sinks;
+                    const bool tail = (key0 + 16 > len && key0 < p.S_cap) || cut;
+                    if (tail) {
+                        const int rows_from = max(len - key0, 0);
+                        for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
+                            const int rrow = idx / (D / 8), ch = idx % (D / 8);
+                            if (rrow >= rows_from || (kSink && !vis.sees(key0 + rrow)))
+                                *reinterpret_cast<uint4 *>(smem + C::OFF_V + st * C::TILE +
+                                                           swz_t<kWide>(warp * 16 + rrow, ch)) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        __syncwarp();
+                    }
+                    // ---- O += P V over this warp's 16 keys ----
+                    {
+                        const int vrow = warp * 16 + (mi & 1) * 8 + rr;
+#pragma unroll
+                        for (int dp = 0; dp < D / 16; ++dp) {
+                            uint32_t b0, b1, b2, b3;
+                            ldmatrix_x4_trans(vb + swz_t<kWide>(vrow, 2 * dp + (mi >> 1)), b0, b1, b2, b3);
+                            mma_m16n8k16(o[2 * dp], pa, b0, b1);
+                            mma_m16n8k16(o[2 * dp + 1], pa, b2, b3);
+                        }
+                    }
+                    if (tail) fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(st));
+            }
+
+            // ---- merge the four warps' states (ring memory is free now) ----
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
+                l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
+            }
+            float *mrg = reinterpret_cast<float *>(smem);
+            // layout: [warp][row 0..15][D] outputs, then m[warp][16], l[warp][16]
+            float *mo = mrg;
+            float *mm = mrg + kConsumers * kMaxGroup * D;
+            float *ml = mm + kConsumers * kMaxGroup;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                const int col = n * 8 + 2 * t;
+                mo[(warp * kMaxGroup + g) * D + col] = o[n][0];
+                mo[(warp * kMaxGroup + g) * D + col + 1] = o[n][1];
+                mo[(warp * kMaxGroup + g + 8) * D + col] = o[n][2];
+                mo[(warp * kMaxGroup + g + 8) * D + col + 1] = o[n][3];
+            }
+            if (t == 0) {
+                mm[warp * kMaxGroup + g] = m_run[0];
+                mm[warp * kMaxGroup + g + 8] = m_run[1];
+                ml[warp * kMaxGroup + g] = l_run[0];
+                ml[warp * kMaxGroup + g + 8] = l_run[1];
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+            if (ok && !*abort_flag && ws_ok) {
+                for (int idx = threadIdx.x; idx < G * D; idx += 32 * kConsumers) {
+                    const int h = idx / D, d = idx % D;
+                    float M = neg_inf();
+#pragma unroll
+                    for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, mm[w * kMaxGroup + h]);
+                    float acc = 0.f, lsum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kConsumers; ++w) {
+                        const float wt = fast_exp2(mm[w * kMaxGroup + h] - M);
+                        acc += wt * mo[(w * kMaxGroup + h) * D + d];
+                        lsum += wt * ml[w * kMaxGroup + h];
+                    }
+                    if constexpr (kCluster) {
+                        part[idx] = acc / lsum;
+                        if (d == 0) part[G * D + h] = M + __log2f(lsum);  // log2 units
+                    } else {
+                        float *dst = ws_base + h * ws_head;
+                        dst[d] = acc / lsum;
+                        if (d == 0) dst[D] = (M + __log2f(lsum)) * 0.69314718055994531f;
+                    }
+                }
+            } else {
+                // A bounded wait ran out: the slice weighs nothing in the combine, so
+                // whatever the workspace held before (another call's partials) never
+                // reaches O.
+                for (int h = threadIdx.x; h < G && ws_ok; h += 32 * kConsumers) {
+                    if constexpr (kCluster) part[G * D + h] = neg_inf();
+                    else ws_base[h * ws_head + D] = neg_inf();
+                }
+            }
         }
+        if (*abort_flag) drain_delay(2000000);
+        __syncthreads();
     }
-    if (*abort_flag) drain_delay(2000000);
-    __syncthreads();
+    if constexpr (kCluster) {
+        cluster_barrier();
+        const uint32_t base = smem_u32(part);
+        for (int idx = split * kDecThreads + threadIdx.x; idx < G * D; idx += p.n_splits * kDecThreads) {
+            const int h = idx / D;
+            float lse[kMaxCluster], v[kMaxCluster], M = neg_inf();
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s)
+                if (s < p.n_splits) {
+                    lse[s] = ld_cluster(base + (G * D + h) * 4, s);
+                    v[s] = ld_cluster(base + idx * 4, s);
+                    M = fmaxf(M, lse[s]);
+                }
+            float o = 0.f, sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s)
+                if (s < p.n_splits && lse[s] != neg_inf()) {  // an empty slice holds anything
+                    const float wt = fast_exp2(lse[s] - M);
+                    sum += wt;
+                    o = fmaf(wt, v[s], o);
+                }
+            p.O[(long long)(b * p.Hq + h0) * D + idx] = __float2bfloat16_rn(sum > 0.f ? o / sum : 0.f);
+        }
+        cluster_barrier();  // no CTA leaves while another reads its partials
+    }
 }
 
 template <int D>
@@ -507,7 +573,7 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-template <int D, bool kPaged, bool kSink>
+template <int D, bool kPaged, bool kSink, bool kCluster>
 attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     using C = DecCfg<D>;
     CUtensorMap tk, tv;
@@ -528,11 +594,12 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
         if ((st = make_tmap_bf16_3d(&tv, a.V, D, a.S_cap, (uint64_t)a.B * a.Hkv, TN)) != ATTN_OK)
             return st;
     }
-    if (kernel_setup(reinterpret_cast<const void *>(decode_split_kernel<D, kPaged, kSink>), C::SMEM_BYTES) !=
+    if (kernel_setup(reinterpret_cast<const void *>(decode_split_kernel<D, kPaged, kSink, kCluster>), C::SMEM_BYTES) !=
         cudaSuccess)
         return ATTN_ERR_CUDA;
     DecParams p;
     p.Q = static_cast<const __nv_bfloat16 *>(a.Q);
+    p.O = static_cast<__nv_bfloat16 *>(a.O);
     p.ws = a.workspace;
     p.lengths = a.lengths;
     p.B = a.B;
@@ -555,18 +622,23 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     while (kPaged && (1 << p.block_shift) < a.block_size) ++p.block_shift;
     // Both kernels are launched with programmatic dependent launch (each waits for
     // its predecessor on the stream before touching global memory).
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster ? a.n_splits : 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_splits, a.Hkv, a.B);
     cfg.blockDim = dim3(kDecThreads, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, decode_split_kernel<D, kPaged, kSink>, tk, tv, p) != cudaSuccess)
+    cfg.numAttrs = kCluster ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, decode_split_kernel<D, kPaged, kSink, kCluster>, tk, tv, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
+    if (kCluster) return ATTN_OK;
     const int BH = a.B * a.Hq;
     cfg.gridDim = dim3((BH + 3) / 4, 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
@@ -579,19 +651,24 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
+bool decode_sinks_in_cluster(int n_splits) { return n_splits <= kMaxCluster; }
+
 size_t decode_workspace_floats(int B, int Hq, int n_splits, int D) {
     return (size_t)B * Hq * n_splits * (D + 4);
 }
 
 attn_status_t launch_decode(const DecodeArgs &a, cudaStream_t stream) {
     if (a.B == 0) return ATTN_OK;
-#define GQA_LAUNCH(DD)                                                         \
-    do {                                                                       \
-        if (a.window > 0)                                                      \
-            return a.block_tables ? launch_decode_d<DD, true, true>(a, stream) \
-                                  : launch_decode_d<DD, false, true>(a, stream); \
-        return a.block_tables ? launch_decode_d<DD, true, false>(a, stream)    \
-                              : launch_decode_d<DD, false, false>(a, stream);  \
+#define GQA_LAUNCH(DD)                                                                  \
+    do {                                                                                \
+        if (a.window > 0 && decode_sinks_in_cluster(a.n_splits))                        \
+            return a.block_tables ? launch_decode_d<DD, true, true, true>(a, stream)    \
+                                  : launch_decode_d<DD, false, true, true>(a, stream);  \
+        if (a.window > 0)                                                               \
+            return a.block_tables ? launch_decode_d<DD, true, true, false>(a, stream)   \
+                                  : launch_decode_d<DD, false, true, false>(a, stream); \
+        return a.block_tables ? launch_decode_d<DD, true, false, false>(a, stream)      \
+                              : launch_decode_d<DD, false, false, false>(a, stream);    \
     } while (0)
     if (a.D == 128) GQA_LAUNCH(128);
     if (a.D == 64) GQA_LAUNCH(64);

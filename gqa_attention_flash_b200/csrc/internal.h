@@ -83,6 +83,10 @@ struct DecodeArgs {
     int window = 0, sinks = 0;
 };
 
+// Whether attn_decode_sinks with that many slices runs as one cluster per (KV head,
+// sequence), which takes no workspace.
+bool decode_sinks_in_cluster(int n_splits);
+
 // Backward of the forward (Tylo.jl `∇attention!`).
 struct BwdArgs {
     void *dQ, *dK, *dV;
