@@ -95,7 +95,11 @@ struct TcParams {
     int B, Hq, Hkv, Sq, Sk, group;
     float scale, scale_log2;
     int causal, window, input_pos;
-    int sinks;  // keys j < sinks stay visible outside the window (kSink only)
+    // kSink only: keys j < sinks stay visible outside the window; key tiles that hold one,
+    // and into how many CTAs the items of such a tile and of another tile are split; fp32
+    // partials of split tiles, a slot per CTA
+    int sinks, sink_tiles, split_sink, split_win;
+    float *part;
     uint64_t wait_limit_ns;
     int *status;
 };
@@ -272,6 +276,21 @@ __device__ __forceinline__ void tc_store_half(uint32_t taddr, __nv_bfloat16 *dst
     }
 }
 
+// The same columns as fp32.
+template <int D>
+__device__ __forceinline__ void tc_store_partial(uint32_t taddr, float *dst, int c0) {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        uint32_t v[32];
+        tmem_ld32(taddr + c0 + c * 32, v);
+        tmem_wait_ld();
+        reg_fence32(v);
+        uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0 + c * 32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d4[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+}
+
 template <int D>
 __device__ __forceinline__ void tc_zero_half(__nv_bfloat16 *dst, int c0) {
     uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
@@ -279,9 +298,26 @@ __device__ __forceinline__ void tc_zero_half(__nv_bfloat16 *dst, int c0) {
     for (int k = 0; k < D / 16; ++k) d4[k] = make_uint4(0, 0, 0, 0);
 }
 
+// Query tiles [qt_lo, qt_lo + n_qt) that hold a row seeing a key of the key tile at kv0.
+template <bool kSink>
+__device__ __forceinline__ int query_tiles(const TcParams &p, int kv0, int k_end, int q_end, int &qt_lo) {
+    int i_lo = 0, i_hi = q_end;
+    if (kv0 >= k_end) i_hi = 0;
+    if (p.causal) i_lo = max(0, kv0 - p.input_pos);
+    if (p.window > 0 && !(kSink && kv0 < p.sinks))
+        i_hi = static_cast<int>(min((long long)i_hi, (long long)kv0 + TB + p.window - p.input_pos));
+    qt_lo = i_lo / TB;
+    return i_hi > i_lo ? (i_hi + TB - 1) / TB - qt_lo : 0;
+}
+
 // ---------------------------------------------------------------------------------
 // dK, dV of one 128-key tile
 // ---------------------------------------------------------------------------------
+// kSink: a tile that holds sinks is seen by every query tile behind it, whatever the
+// window, so it may have many times another tile's items.  Such tiles go first, and where
+// their items are still more than an SM's share they are split over CTAs, as are all tiles
+// when there are fewer than SMs; split CTAs leave fp32 partials that
+// bwd_dkdv_reduce_kernel adds up in a fixed order.
 template <int D, bool kSink>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -298,23 +334,42 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8 * i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pairs = p.Hkv * p.B, n_kt = (p.Sk + TB - 1) / TB;
-    const int G = min(4, pairs), full = pairs / G;
-    const int chunk = min(static_cast<int>(blockIdx.x / (G * n_kt)), full);
-    const int size = chunk < full ? G : pairs - full * G;
-    const int local = static_cast<int>(blockIdx.x) - chunk * G * n_kt;
-    const int kt = local / size, pair = chunk * G + local % size;
+    const int pairs = p.Hkv * p.B;
+    int n_kt = (p.Sk + TB - 1) / TB, bid = static_cast<int>(blockIdx.x);
+    int split = 1, part_i = 0, kt, pair;  // this CTA's share part_i of the tile's `split`
+    bool sink_cta = false;
+    if constexpr (kSink) {
+        const int n_sink = p.sink_tiles * pairs * p.split_sink;
+        sink_cta = bid < n_sink;
+        split = sink_cta ? p.split_sink : p.split_win;
+        if (!sink_cta) bid -= n_sink;
+        part_i = bid % split;
+        bid /= split;
+        n_kt -= p.sink_tiles;
+    }
+    if (sink_cta) {
+        kt = bid / pairs;
+        pair = bid % pairs;
+    } else {
+        const int G = min(4, pairs), full = pairs / G;
+        const int chunk = min(bid / (G * n_kt), full);
+        const int size = chunk < full ? G : pairs - full * G;
+        const int local = bid - chunk * G * n_kt;
+        kt = local / size + (kSink ? p.sink_tiles : 0);
+        pair = chunk * G + local % size;
+    }
     const int hkv = pair % p.Hkv, b = pair / p.Hkv;
     const int kv0 = kt * TB;
     int k_end, q_end;
     tc_lengths(p, b, k_end, q_end);
-    // query tiles that hold a row seeing a key of this tile
-    int i_lo = 0, i_hi = q_end;
-    if (kv0 >= k_end) i_hi = 0;
-    if (p.causal) i_lo = max(0, kv0 - p.input_pos);
-    if (p.window > 0 && !(kSink && kv0 < p.sinks)) i_hi = static_cast<int>(min((long long)i_hi, (long long)kv0 + TB + p.window - p.input_pos));
-    const int qt_lo = i_lo / TB, qt_hi = i_hi > i_lo ? (i_hi + TB - 1) / TB : qt_lo;
-    const int n_qt = qt_hi - qt_lo, n_it = p.group * n_qt;
+    int qt_lo;
+    const int n_qt = query_tiles<kSink>(p, kv0, k_end, q_end, qt_lo);
+    int n_it = p.group * n_qt, it0 = 0;  // items [it0, it0 + n_it) of (query head, query tile)
+    if (kSink && split > 1) {
+        const int per = (n_it + split - 1) / split;
+        it0 = min(part_i * per, n_it);
+        n_it = min(per, n_it - it0);
+    }
 
     const uint32_t tmem = tc_setup<C>(smem, sbase);
 
@@ -340,8 +395,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             for (int it = 0; it < n_it; ++it) {
                 const int st = it % C::NS, use = it / C::NS;
-                const int hq = hkv * p.group + it / n_qt;
-                const int q0 = (qt_lo + it % n_qt) * TB;
+                const int hq = hkv * p.group + (it0 + it) / n_qt;
+                const int q0 = (qt_lo + (it0 + it) % n_qt) * TB;
                 const long long qrow = (long long)(b * p.Hq + hq) * p.Sq;
                 // checked build: this item's Q / dO tiles and LSE / delta rows exist
                 if (!in_range(hq < p.Hq && box_ok(0, q0, b * p.Hq + hq, D, p.Sq, (long long)p.B * p.Hq,
@@ -453,7 +508,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 break;
             }
             tc_fence_after();
-            const int q0 = (qt_lo + it % n_qt) * TB;
+            const int q0 = (qt_lo + (it0 + it) % n_qt) * TB;
             const float *rows = reinterpret_cast<const float *>(smem + C::stage(st) + 2 * C::TILE);
             int lo, hi;
             cols_of_key<kSink>(p, j, q0, k_end, q_end, lo, hi);
@@ -540,7 +595,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const bool have = ok && n_it > 0 &&
                           warp_wait(bar(C::BAR_DONE), 0, abort_flag, p.wait_limit_ns, p.status);
         const long long krow = (long long)(b * p.Hkv + hkv) * p.Sk + j;
-        if (have) {
+        if (kSink && split > 1) {
+            if (have) {
+                tc_fence_after();
+                float *dst = p.part + (long long)blockIdx.x * (2 * TB * D) + r * D;
+                tc_store_partial<D>(trow + C::COL_A, dst, half * (D / 2));
+                tc_store_partial<D>(trow + C::COL_B, dst + TB * D, half * (D / 2));
+            }
+        } else if (have) {
             tc_fence_after();
             tc_store_half<D>(trow + C::COL_A, p.dV + krow * D, half * (D / 2), 1.f, j < p.Sk,
                              j < k_end);
@@ -552,6 +614,61 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
     }
     tc_teardown<C>(smem, tmem);
+}
+
+// Sum of a split tile's partials: 16 rows of dV and dK per block, 8 columns per thread and
+// step, the parts in increasing order.  blockIdx.x: (tile, pair) in the order of
+// bwd_dkdv_tc_kernel's CTAs (tiles without a split are not part of the grid).
+template <int D>
+__global__ void __launch_bounds__(256) bwd_dkdv_reduce_kernel(const TcParams p) {
+    constexpr int kRows = 16, kVec = D / 8;
+    const int pairs = p.Hkv * p.B;
+    int n_kt = (p.Sk + TB - 1) / TB, bid = static_cast<int>(blockIdx.x), kt, pair, split, slot;
+    const int n_sink = p.split_sink > 1 ? p.sink_tiles * pairs : 0;
+    if (bid < n_sink) {
+        split = p.split_sink;
+        slot = bid * split;
+        kt = bid / pairs;
+        pair = bid % pairs;
+    } else {
+        bid -= n_sink;
+        split = p.split_win;
+        slot = p.sink_tiles * pairs * p.split_sink + bid * split;
+        n_kt -= p.sink_tiles;
+        const int G = min(4, pairs), full = pairs / G;
+        const int chunk = min(bid / (G * n_kt), full);
+        const int size = chunk < full ? G : pairs - full * G;
+        const int local = bid - chunk * G * n_kt;
+        kt = local / size + p.sink_tiles;
+        pair = chunk * G + local % size;
+    }
+    const int hkv = pair % p.Hkv, b = pair / p.Hkv, kv0 = kt * TB;
+    int k_end, q_end, qt_lo;
+    tc_lengths(p, b, k_end, q_end);
+    const int n_it = p.group * query_tiles<true>(p, kv0, k_end, q_end, qt_lo);
+    const int per = (n_it + split - 1) / split;
+    const int parts = n_it > 0 ? (n_it + per - 1) / per : 0;  // those that had an item
+    for (int x = threadIdx.x; x < 2 * kRows * kVec; x += 256) {
+        const int which = x / (kRows * kVec), r = blockIdx.y * kRows + x / kVec % kRows, c = x % kVec;
+        const int j = kv0 + r;
+        if (j >= p.Sk) continue;
+        float acc[8] = {};
+        const float *src = p.part + ((long long)slot * 2 + which) * (TB * D) + r * D + c * 8;
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float4 a = *reinterpret_cast<const float4 *>(src + (long long)s * (2 * TB * D));
+            const float4 d = *reinterpret_cast<const float4 *>(src + (long long)s * (2 * TB * D) + 4);
+            acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+            acc[4] += d.x; acc[5] += d.y; acc[6] += d.z; acc[7] += d.w;
+        }
+        const float mul = which ? p.scale : 1.f;
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (j < k_end && parts > 0)
+            o = make_uint4(pack_bf16x2(acc[0] * mul, acc[1] * mul), pack_bf16x2(acc[2] * mul, acc[3] * mul),
+                           pack_bf16x2(acc[4] * mul, acc[5] * mul), pack_bf16x2(acc[6] * mul, acc[7] * mul));
+        __nv_bfloat16 *dst = which ? p.dK : p.dV;
+        *reinterpret_cast<uint4 *>(dst + ((long long)(b * p.Hkv + hkv) * p.Sk + j) * D + c * 8) = o;
+    }
 }
 
 // ---------------------------------------------------------------------------------
@@ -865,6 +982,67 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     const int n_qt = (a.Sq + TB - 1) / TB;
     const long long grid = (long long)n_qt * a.Hq * a.B;
     if (grid > 0x7fffffffll) return ATTN_ERR_INVALID;
+    const int n_kt = (a.Sk + TB - 1) / TB, pairs = a.Hkv * a.B;
+    long long grid_kv = (long long)n_kt * pairs, reduce = 0;
+    void *part = nullptr;
+    p.part = nullptr;
+    p.sink_tiles = 0;
+    p.split_sink = p.split_win = 1;
+    int n_sm = 148;
+    if constexpr (kSink) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n_sm < 1)
+            return ATTN_ERR_CUDA;
+        // Items (query head, query tile) of a tile with sinks and of another one, lengths
+        // aside.  A CTA of more items than an SM's share (and than 4: a partial costs about
+        // as much as one item) is split; tiles without sinks only where there are fewer than
+        // SMs (B2 Hq8 S1000 w200 D64: 58 -> 27 us a call).
+        const long long sink_keys = a.sinks < a.Sk ? a.sinks : a.Sk;
+        p.sink_tiles = static_cast<int>((sink_keys + TB - 1) / TB);
+        const long long n_s = (long long)p.group * n_qt;
+        const long long w_qt = ((long long)a.window + TB - 2) / TB + 2;
+        const long long n_w = (long long)p.group * (w_qt < n_qt ? w_qt : n_qt);
+        const long long others = (long long)(n_kt - p.sink_tiles) * pairs;
+        const long long share = (p.sink_tiles * pairs * n_s + others * n_w + n_sm - 1) / n_sm;
+        long long most = share > 4 ? share : 4;
+        if (grid_kv < n_sm) p.split_win = static_cast<int>((n_w + most - 1) / most);
+        const long long w_len = (n_w + p.split_win - 1) / p.split_win;
+        if (others > 0 && w_len > most) most = w_len;
+        p.split_sink = static_cast<int>((n_s + most - 1) / most);
+        const long long sink_ctas = (long long)p.sink_tiles * pairs * p.split_sink;
+        grid_kv = sink_ctas + others * p.split_win;
+        if (p.split_sink > 1) reduce += (long long)p.sink_tiles * pairs;
+        if (p.split_win > 1) reduce += others;
+        if (reduce > 0) {
+            const long long slots = p.split_win > 1 ? grid_kv : sink_ctas;
+            if (workspace_alloc(&part, (size_t)slots * 2 * TB * D * sizeof(float), stream) != cudaSuccess)
+                return ATTN_ERR_CUDA;
+            p.part = static_cast<float *>(part);
+        }
+    }
+    if (grid_kv > 0x7fffffffll) return ATTN_ERR_INVALID;
+    auto launch_dq = [&](cudaStream_t s) -> bool {
+        bwd_dq_tc_kernel<D, kSink><<<static_cast<unsigned>(grid), kThreadsTc, DqCfg<D>::SMEM, s>>>(
+            tq, tk, tv, tdo, p, n_qt);
+        return cudaGetLastError() == cudaSuccess;
+    };
+    auto launch_dkdv = [&]() -> bool {
+        if (a.Sk == 0) return true;
+        bwd_dkdv_tc_kernel<D, kSink><<<static_cast<unsigned>(grid_kv), kThreadsTc, C::SMEM, stream>>>(
+            tq, tk, tv, tdo, p);
+        if (cudaGetLastError() != cudaSuccess) return false;
+        if constexpr (kSink) {
+            if (reduce > 0) {
+                bwd_dkdv_reduce_kernel<D><<<dim3(static_cast<unsigned>(reduce), TB / 16), 256, 0, stream>>>(p);
+                if (cudaGetLastError() != cudaSuccess) return false;
+            }
+            if (part && cudaFreeAsync(part, stream) != cudaSuccess) return false;
+        }
+        return true;
+    };
+    if (kSink && grid < n_sm && grid_kv < 2 * n_sm)  // too little work for the events' cost
+        return launch_dq(stream) && launch_dkdv() ? ATTN_OK : ATTN_ERR_CUDA;
     // dK/dV and dQ are independent: run dQ on a side stream so that each kernel's
     // last wave overlaps the other's work.
     SideStream *ss = side_stream();
@@ -873,16 +1051,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     if (cudaEventRecord(ss->fork, stream) != cudaSuccess ||
         cudaStreamWaitEvent(ss->s, ss->fork, 0) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    bwd_dq_tc_kernel<D, kSink><<<static_cast<unsigned>(grid), kThreadsTc, DqCfg<D>::SMEM, ss->s>>>(tq, tk, tv, tdo, p,
-                                                                                    n_qt);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    if (a.Sk > 0) {
-        const long long grid_kv = (long long)((a.Sk + TB - 1) / TB) * a.Hkv * a.B;
-        if (grid_kv > 0x7fffffffll) return ATTN_ERR_INVALID;
-        bwd_dkdv_tc_kernel<D, kSink><<<static_cast<unsigned>(grid_kv), kThreadsTc, C::SMEM, stream>>>(
-            tq, tk, tv, tdo, p);
-        if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    }
+    if (!launch_dq(ss->s) || !launch_dkdv()) return ATTN_ERR_CUDA;
     if (cudaEventRecord(ss->join, ss->s) != cudaSuccess ||
         cudaStreamWaitEvent(stream, ss->join, 0) != cudaSuccess)
         return ATTN_ERR_CUDA;
