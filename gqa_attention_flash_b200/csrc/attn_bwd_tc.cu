@@ -514,6 +514,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             cols_of_key<kSink>(p, j, q0, k_end, q_end, lo, hi);
             lo -= cb;
             hi -= cb;
+            // tiles inside every row's range (all but the diagonal's and the window's edge)
+            // need no selection: the warp's columns are all visible (LLM causal backward 1.93
+            // -> 1.79 ms, with a window of 1024 and 4 sinks 1.19 -> 1.14 ms, bitwise the same)
+            const bool inner = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
             float pr[64];
             {
                 uint32_t sv[2][32];
@@ -540,10 +544,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                                                      __uint_as_float(sv[x >> 5][(x + 1) & 31])),
                                              sl2x2, h ? f2_pack(l.z, l.w) : f2_pack(l.x, l.y)),
                                       x0, x1);
-                            const float v0 = fast_exp2(x0), v1 = fast_exp2(x1);
-                            pr[x] = (x >= lo && x < hi) ? v0 : 0.f;
-                            pr[x + 1] = (x + 1 >= lo && x + 1 < hi) ? v1 : 0.f;
+                            pr[x] = fast_exp2(x0);
+                            pr[x + 1] = fast_exp2(x1);
                         }
+                    }
+                    if (!inner) {
+#pragma unroll
+                        for (int x = 32 * c; x < 32 * c + 32; ++x) pr[x] = (x >= lo && x < hi) ? pr[x] : 0.f;
                     }
                     uint32_t pk[16];
 #pragma unroll
@@ -851,6 +858,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             clo -= cb;
             chi -= cb;
             const int cs = p.sinks - kv0 - cb;  // kSink: columns below it are sinks
+            const bool inner = __all_sync(0xffffffffu, clo <= 0 && chi >= 64);  // as in dK / dV
             float pr[64];
             {
                 uint32_t sv[2][32];
@@ -867,9 +875,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                                              __uint_as_float(sv[x >> 5][(x + 1) & 31])),
                                      sl2x2, nl2),
                               x0, x1);
-                    const float v0 = fast_exp2(x0), v1 = fast_exp2(x1);
-                    pr[x] = ((x >= clo || (kSink && x < cs)) && x < chi) ? v0 : 0.f;
-                    pr[x + 1] = ((x + 1 >= clo || (kSink && x + 1 < cs)) && x + 1 < chi) ? v1 : 0.f;
+                    pr[x] = fast_exp2(x0);
+                    pr[x + 1] = fast_exp2(x1);
+                }
+                if (!inner) {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        pr[x] = ((x >= clo || (kSink && x < cs)) && x < chi) ? pr[x] : 0.f;
                 }
             }
             if (!warp_wait(bar(C::BAR_DPFULL), g & 1, abort_flag, p.wait_limit_ns, p.status)) {

@@ -50,9 +50,11 @@ __device__ __forceinline__ long long pool_row(const int32_t *bt, int pos, int sh
 // ---------------------------------------------------------------------------------
 // append: row t of sequence b to position start[b] + t
 // ---------------------------------------------------------------------------------
-// One thread moves 16 bytes of K and of V.  The source's innermost axes are (t, d), so a
-// warp reads consecutive bytes and writes whole rows of one head (2 D bytes each).
+// A thread moves kAppendUnroll x 16 bytes of K and of V, all loads in flight at once.  The
+// source's innermost axes are (t, d), so a warp reads consecutive bytes and writes whole
+// rows of one head (2 D bytes each).
 constexpr int kAppendThreads = 128;
+constexpr int kAppendUnroll = 4;
 
 struct AppendParams {
     uint4 *K, *V;
@@ -68,8 +70,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     const int chunk = static_cast<int>(blockIdx.x % p.chunks);
     const long long bh = blockIdx.x / p.chunks;
     const int h = static_cast<int>(bh % p.Hkv), b = static_cast<int>(bh / p.Hkv);
-    const long long idx = (long long)chunk * kAppendThreads + threadIdx.x;
-    const int t = static_cast<int>(idx / p.vec), c = static_cast<int>(idx % p.vec);
     int n = p.T;
     if (p.n_new) {
         n = p.n_new[b];
@@ -78,22 +78,35 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             n = p.T;
         }
     }
-    if (t >= n) return;
-    const long long pos = (long long)p.start[b] + t;
-    if (pos < 0 || pos >= p.capacity) {
-        record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-        return;
+    const long long start = p.start[b];
+    const int32_t *bt = p.tables + (long long)b * p.max_blocks;
+    uint4 k[kAppendUnroll], v[kAppendUnroll];
+    long long dst[kAppendUnroll];
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u) {
+        const long long idx =
+            ((long long)chunk * kAppendUnroll + u) * kAppendThreads + threadIdx.x;
+        const int t = static_cast<int>(idx / p.vec), c = static_cast<int>(idx % p.vec);
+        dst[u] = -1;
+        if (t >= n) continue;
+        const long long pos = start + t;
+        long long row = -1;
+        if (pos >= 0 && pos < p.capacity) row = pool_row(bt, static_cast<int>(pos), p.shift, p.num_blocks);
+        if (row < 0) {
+            record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+            continue;
+        }
+        const long long src = (bh * p.T + t) * p.vec + c;
+        k[u] = p.Kn[src];
+        v[u] = p.Vn[src];
+        dst[u] = (row * p.Hkv + h) * p.vec + c;
     }
-    const long long row =
-        pool_row(p.tables + (long long)b * p.max_blocks, static_cast<int>(pos), p.shift, p.num_blocks);
-    if (row < 0) {
-        record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-        return;
-    }
-    const long long src = (bh * p.T + t) * p.vec + c, dst = (row * p.Hkv + h) * p.vec + c;
-    const uint4 k = p.Kn[src], v = p.Vn[src];
-    p.K[dst] = k;
-    p.V[dst] = v;
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u)
+        if (dst[u] >= 0) {
+            p.K[dst[u]] = k[u];
+            p.V[dst[u]] = v[u];
+        }
 }
 
 // ---------------------------------------------------------------------------------
@@ -101,12 +114,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 // ---------------------------------------------------------------------------------
 // In place.  keep is ascending, so keep[k] >= k: a row that step k writes is the source
 // of no later step, and a block may move its slice of the columns in steps of kStep rows
-// (read the step, wait for the block, write it), with nothing but its own order to keep.
+// (read the step, wait for the block, write it), with nothing but its own order to keep; a
+// step may even be read before the one before it is written.  So two steps are in flight,
+// their rows looked up in shared memory (B4, half of 2048 to 4096 rows of 2 KB kept:
+// 35 us with one step in flight and the lookups in its way, 19 us so).
 constexpr int kCompactThreads = 256;
-constexpr int kSliceVec = 8;                                  // 16-byte words of a row per block
+constexpr int kSliceVec = 4;                                  // 16-byte words of a row per block
 constexpr int kStepRows = kCompactThreads / kSliceVec;        // rows per pass of the block
 constexpr int kPasses = 4;
 constexpr int kStep = kStepRows * kPasses;
+constexpr int kCompactList = 2048;                            // rows looked up at a time
 
 struct CompactParams {
     uint4 *K, *V;
@@ -117,6 +134,7 @@ struct CompactParams {
 };
 
 __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactParams p) {
+    __shared__ int rows_from[kCompactList], rows_to[kCompactList];
     pdl_wait();
     const int slice = static_cast<int>(blockIdx.x % p.slices);
     const int b = static_cast<int>(blockIdx.x / p.slices);
@@ -140,9 +158,15 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
         const int x = keep[k];
         const int before = k > 0 ? keep[k - 1] : -1;
         bad = x <= before || x < 0 || base + x >= p.capacity;
-        if (!bad)
-            bad = pool_row(bt, static_cast<int>(base + x), p.shift, p.num_blocks) < 0 ||
-                  pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks) < 0;
+        if (!bad) {
+            const long long from = pool_row(bt, static_cast<int>(base + x), p.shift, p.num_blocks);
+            const long long to = pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks);
+            bad = from < 0 || to < 0;
+            if (k < kCompactList) {
+                rows_from[k] = static_cast<int>(from);
+                rows_to[k] = static_cast<int>(to);
+            }
+        }
     }
     if (__syncthreads_or(bad)) {
         if (report) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
@@ -150,24 +174,40 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
     }
     const int col = slice * kSliceVec + threadIdx.x % kSliceVec;
     const int r = threadIdx.x / kSliceVec;
-    for (int k0 = 0; k0 < n; k0 += kStep) {
-        uint4 v[kPasses];
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int k = k0 + i * kStepRows + r;
-            if (k < n && col < p.row_vec)
-                v[i] = pool[pool_row(bt, static_cast<int>(base + keep[k]), p.shift, p.num_blocks) *
-                                p.row_vec + col];
+    for (int l0 = 0; l0 < n; l0 += kCompactList) {
+        const int m = min(n - l0, kCompactList);  // rows l0 .. l0 + m - 1 of the list
+        if (l0 > 0) __syncthreads();  // the first rows are there from the check
+        for (int k = threadIdx.x; k < m && l0 > 0; k += kCompactThreads) {
+            rows_from[k] = static_cast<int>(
+                pool_row(bt, static_cast<int>(base + keep[l0 + k]), p.shift, p.num_blocks));
+            rows_to[k] =
+                static_cast<int>(pool_row(bt, static_cast<int>(base + l0 + k), p.shift, p.num_blocks));
         }
-        __syncthreads();
+        if (l0 > 0) __syncthreads();
+        uint4 v[2][kPasses];
+        auto read = [&](uint4 (&x)[kPasses], int k0) {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int k = k0 + i * kStepRows + r;
-            if (k < n && col < p.row_vec)
-                pool[pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks) * p.row_vec + col] =
-                    v[i];
+            for (int i = 0; i < kPasses; ++i) {
+                const int k = k0 + i * kStepRows + r;
+                if (k < m && col < p.row_vec) x[i] = pool[(long long)rows_from[k] * p.row_vec + col];
+            }
+        };
+        auto write = [&](const uint4 (&x)[kPasses], int k0) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int k = k0 + i * kStepRows + r;
+                if (k < m && col < p.row_vec) pool[(long long)rows_to[k] * p.row_vec + col] = x[i];
+            }
+        };
+        read(v[0], 0);
+        for (int k0 = 0; k0 < m; k0 += 2 * kStep) {
+            read(v[1], k0 + kStep);
+            __syncthreads();  // every read of step k0 is done
+            write(v[0], k0);
+            read(v[0], k0 + 2 * kStep);
+            __syncthreads();
+            write(v[1], k0 + kStep);
         }
-        __syncthreads();
     }
 }
 
@@ -499,7 +539,8 @@ attn_status_t launch_cache_append(const CacheArgs &a, cudaStream_t stream) {
     p.capacity = (long long)a.max_blocks * a.block_size;
     p.status = device_status_word();
     if (!p.status) return ATTN_ERR_CUDA;
-    const long long chunks = ((long long)a.T * p.vec + kAppendThreads - 1) / kAppendThreads;
+    constexpr int kPer = kAppendThreads * kAppendUnroll;
+    const long long chunks = ((long long)a.T * p.vec + kPer - 1) / kPer;
     const long long grid = chunks * a.B * a.Hkv;
     if (grid > 0x7fffffffll) return ATTN_ERR_INVALID;
     p.chunks = static_cast<int>(chunks);
