@@ -27,6 +27,8 @@ __global__ void __launch_bounds__(256)
     bwd_delta_kernel(const __nv_bfloat16 *dO, const __nv_bfloat16 *O, float *delta, long long rows) {
     constexpr int kTpr = D / 8;          // threads per row
     constexpr int kRpb = 256 / kTpr;     // rows per block
+    // the next kernel may start its set-up (it waits for this one before it reads)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long r = (long long)blockIdx.x * kRpb + threadIdx.x / kTpr;
     const int c = threadIdx.x % kTpr;
     float acc = 0.f;

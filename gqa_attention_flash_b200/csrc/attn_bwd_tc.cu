@@ -298,6 +298,13 @@ __device__ __forceinline__ void tc_zero_half(__nv_bfloat16 *dst, int c0) {
     for (int k = 0; k < D / 16; ++k) d4[k] = make_uint4(0, 0, 0, 0);
 }
 
+// Programmatic dependent launch on one stream (kSink, small calls): nothing that the
+// kernels before write is touched before this.
+__device__ __forceinline__ void dependent_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Query tiles [qt_lo, qt_lo + n_qt) that hold a row seeing a key of the key tile at kv0.
 template <bool kSink>
 __device__ __forceinline__ int query_tiles(const TcParams &p, int kv0, int k_end, int q_end, int &qt_lo) {
@@ -372,6 +379,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
 
     const uint32_t tmem = tc_setup<C>(smem, sbase);
+    if constexpr (kSink) dependent_wait();
 
     if (warp == kWarpTmaB) {
         // ===================== TMA producer =====================
@@ -651,6 +659,7 @@ __global__ void __launch_bounds__(256) bwd_dkdv_reduce_kernel(const TcParams p) 
     }
     const int hkv = pair % p.Hkv, b = pair / p.Hkv, kv0 = kt * TB;
     int k_end, q_end, qt_lo;
+    dependent_wait();
     tc_lengths(p, b, k_end, q_end);
     const int n_it = p.group * query_tiles<true>(p, kv0, k_end, q_end, qt_lo);
     const int per = (n_it + split - 1) / split;
@@ -751,6 +760,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     auto key_tile = [&](int g) -> int { return kSink && g < n_s ? g : lo + g - (kSink ? n_s : 0); };
 
     const uint32_t tmem = tc_setup<C>(smem, sbase);
+    if constexpr (kSink) dependent_wait();
 
     if (warp == kWarpTmaB) {
         // ===================== TMA producer =====================
@@ -1034,27 +1044,39 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
         }
     }
     if (grid_kv > 0x7fffffffll) return ATTN_ERR_INVALID;
+    // Too little work for the events' cost: one stream, each kernel a programmatic dependent
+    // of the one before.
+    const bool one_stream = kSink && grid < n_sm && grid_kv < 2 * n_sm;
+    auto launch = [&](auto kernel, dim3 blocks, int threads, int smem, cudaStream_t s, auto... args) -> bool {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = blocks;
+        cfg.blockDim = dim3(threads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = one_stream ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+    };
     auto launch_dq = [&](cudaStream_t s) -> bool {
-        bwd_dq_tc_kernel<D, kSink><<<static_cast<unsigned>(grid), kThreadsTc, DqCfg<D>::SMEM, s>>>(
-            tq, tk, tv, tdo, p, n_qt);
-        return cudaGetLastError() == cudaSuccess;
+        return launch(bwd_dq_tc_kernel<D, kSink>, dim3(static_cast<unsigned>(grid)), kThreadsTc,
+                      DqCfg<D>::SMEM, s, tq, tk, tv, tdo, p, n_qt);
     };
     auto launch_dkdv = [&]() -> bool {
         if (a.Sk == 0) return true;
-        bwd_dkdv_tc_kernel<D, kSink><<<static_cast<unsigned>(grid_kv), kThreadsTc, C::SMEM, stream>>>(
-            tq, tk, tv, tdo, p);
-        if (cudaGetLastError() != cudaSuccess) return false;
+        bool ok = launch(bwd_dkdv_tc_kernel<D, kSink>, dim3(static_cast<unsigned>(grid_kv)), kThreadsTc,
+                         C::SMEM, stream, tq, tk, tv, tdo, p);
         if constexpr (kSink) {
-            if (reduce > 0) {
-                bwd_dkdv_reduce_kernel<D><<<dim3(static_cast<unsigned>(reduce), TB / 16), 256, 0, stream>>>(p);
-                if (cudaGetLastError() != cudaSuccess) return false;
-            }
-            if (part && cudaFreeAsync(part, stream) != cudaSuccess) return false;
+            if (ok && reduce > 0)
+                ok = launch(bwd_dkdv_reduce_kernel<D>, dim3(static_cast<unsigned>(reduce), TB / 16), 256, 0,
+                            stream, p);
+            if (part && cudaFreeAsync(part, stream) != cudaSuccess) ok = false;
         }
-        return true;
+        return ok;
     };
-    if (kSink && grid < n_sm && grid_kv < 2 * n_sm)  // too little work for the events' cost
-        return launch_dq(stream) && launch_dkdv() ? ATTN_OK : ATTN_ERR_CUDA;
+    if (one_stream) return launch_dq(stream) && launch_dkdv() ? ATTN_OK : ATTN_ERR_CUDA;
     // dK/dV and dQ are independent: run dQ on a side stream so that each kernel's
     // last wave overlaps the other's work.
     SideStream *ss = side_stream();
