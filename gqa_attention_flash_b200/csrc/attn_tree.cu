@@ -325,13 +325,13 @@ __device__ __forceinline__ void tree_produce(const TreeParams &p, uint8_t *smem,
                                             p.status)) {
                     ok = false;
                 } else {
-                    const int row0 = (w.b * p.Hq + w.hkv * (p.Hq / p.Hkv)) * p.T + w.rt * C::ROWS;
                     const int n_q = C::NQ == 2 && tree_rows<C>(p, w.rt, 1) > 0 ? 2 : 1;
                     mbar_arrive_expect_tx(bar(C::BAR_QFULL), n_q * C::QTILE);
                     for (int t = 0; t < n_q; ++t)
                         for (int c = 0; c < C::NBOX; ++c)
                             tma_load_3d(sbase + C::OFF_Q + t * C::QTILE + c * C::QBOX, tmQ,
-                                        bar(C::BAR_QFULL), c * 64, row0 + t * C::RQ, 0);
+                                        bar(C::BAR_QFULL), c * 64, w.rt * C::ROWS + t * C::RQ,
+                                        w.b * p.Hkv + w.hkv);
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -799,7 +799,7 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
     CUtensorMap tq, tk, tv;
     attn_status_t st;
     const uint64_t rows = (uint64_t)a.num_blocks * a.block_size;
-    if ((st = make_tmap_bf16_3d(&tq, a.Q, D, (uint64_t)a.B * a.Hq * a.T, 1, C::RQ)) != ATTN_OK ||
+    if ((st = make_tmap_bf16_3d(&tq, a.Q, D, p.R, (uint64_t)a.B * a.Hkv, C::RQ)) != ATTN_OK ||
         (st = make_tmap_bf16_paged_groups(&tk, a.K, D, a.Hkv, rows, p.box_rows)) != ATTN_OK ||
         (st = make_tmap_bf16_paged_groups(&tv, a.V, D, a.Hkv, rows, p.box_rows)) != ATTN_OK)
         return st;
