@@ -15,10 +15,13 @@
 // the time is HBM's: transposed products (keys as M, N = 64 rows) halve the tensor work of
 // 64 rows and ran no faster (B64 x 16 drafts: 768 us against 732).
 //
-// Work.  The 128-key tiles of all (sequence, KV head, row pass) segments form one list
-// that the CTAs share out in equal runs, so ragged lengths leave no SM idle and a single
-// long sequence uses all of them.  A segment that ends up in several CTAs leaves partial
-// states (max, sum, unnormalised O, fp32) in a workspace; tree_combine_kernel merges them.
+// Work.  The 128-key tiles of all (sequence, KV head, row pass) segments form a list that
+// the CTAs share out in equal runs, so ragged lengths leave no SM idle and a single long
+// sequence uses all of them.  A segment that ends up in several CTAs leaves partial states
+// (max, sum, unnormalised O, fp32) in a workspace; tree_combine_kernel merges them.
+// The (KV head, row pass) pairs run in lanes, one CTA each over the same runs: the heads'
+// rows of a token are neighbours in HBM, and the passes' K / V are the same, so that what
+// stands together is read together.
 //
 // 12 warps: 0-3 and 4-7 softmax (one row per thread = TMEM lane), 8 and 10 TMA producers,
 // 9 MMA issuer, 11 idle; registers move from 8-11 to the softmax warps as in the forward.
@@ -85,7 +88,10 @@ struct TreeParams {
     float *ws;
     const int32_t *tables, *ctx, *parents, *drafts;
     int B, Hq, Hkv, T, R, n_rt, max_blocks, num_blocks, shift, box_rows;
-    int n_cta;
+    // (KV head, row pass) pair q runs in lane q % lanes, as segment q / lanes of each
+    // sequence; a lane's list of segs segments per sequence is cut into n_run runs, run k
+    // of lane l being CTA k * lanes + l
+    int lanes, segs, n_run;
     float scale_log2;
     uint64_t wait_limit_ns;
     int *status;
@@ -167,7 +173,7 @@ struct TreeWalk {
 
     __device__ __forceinline__ bool next(const TreeParams &p) {
         if (f >= f_end) return false;
-        const long long H = (long long)p.Hkv * p.n_rt;
+        const long long H = p.segs;
         while (f >= (pre + len.nt) * H) {
             pre += len.nt;
             len = tree_lens(p, ++b, false);
@@ -175,8 +181,9 @@ struct TreeWalk {
         const long long rem = f - pre * H;
         const int seg = static_cast<int>(rem / len.nt);
         t_a = static_cast<int>(rem - (long long)seg * len.nt);
-        hkv = seg / p.n_rt;
-        rt = seg - hkv * p.n_rt;
+        const int q = seg * p.lanes + static_cast<int>(blockIdx.x % p.lanes);
+        hkv = q / p.n_rt;
+        rt = q - hkv * p.n_rt;
         t_b = static_cast<int>(min((long long)len.nt, t_a + f_end - f));
         f += t_b - t_a;
         return true;
@@ -212,9 +219,9 @@ __device__ __forceinline__ bool tree_setup(const TreeParams &p, uint8_t *smem, T
     long long mine = 0, total;
     for (int b = b0; b < b1; ++b) mine += tree_lens(p, b, blockIdx.x == 0).nt;
     const long long before = block_scan(mine, warp_sums, total);
-    const long long H = (long long)p.Hkv * p.n_rt;
-    const long long share = (total * H + p.n_cta - 1) / p.n_cta;
-    w.f_first = w.f = blockIdx.x * share;
+    const long long H = p.segs;
+    const long long share = (total * H + p.n_run - 1) / p.n_run;
+    w.f_first = w.f = blockIdx.x / p.lanes * share;
     w.f_end = min(total * H, w.f + share);
     if (w.f >= w.f_end) return false;
     if (before * H <= w.f && w.f < (before + mine) * H) {
@@ -707,8 +714,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     const long long before = block_scan(mine, warp_sums, total);
     if (b >= b0 && b < b1) found = before + upto;
     __syncthreads();
-    const long long H = (long long)p.Hkv * p.n_rt;
-    const long long share = (total * H + p.n_cta - 1) / p.n_cta;
+    const long long H = p.segs;
+    const long long share = (total * H + p.n_run - 1) / p.n_run;
     const TreeLens len = tree_lens(p, b, false);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int k = warp; k < rows_per_block; k += kCombineThreads / 32) {
@@ -719,14 +726,15 @@ __global__ void __launch_bounds__(kCombineThreads)
         float inv = 0.f;
         if (len.nt > 0) {
             const int rt = row / C::ROWS, prow = row - rt * C::ROWS;
-            const long long f0 = found * H + (long long)(hkv * p.n_rt + rt) * len.nt, f1 = f0 + len.nt;
+            const int q = hkv * p.n_rt + rt, lane_q = q % p.lanes;
+            const long long f0 = found * H + (long long)(q / p.lanes) * len.nt, f1 = f0 + len.nt;
             const int c0 = static_cast<int>(f0 / share), n = static_cast<int>((f1 - 1) / share) - c0 + 1;
             if (n == 1) continue;  // one CTA wrote the row
-            const float *ws0 = p.ws + (long long)(2 * c0) * C::WS;
-            // piece i of the segment: slot 2 (c0 + i), or 2 c0 + 1 when it closes c0's run
+            // piece i of the segment, in run c0 + i of its lane: the first slot of that CTA, or
+            // the second where the piece closes run c0
             const int odd = f0 > c0 * share ? 1 : 0;
             auto piece = [&](int i) -> const float * {
-                return ws0 + (long long)(2 * i + (i == 0 ? odd : 0)) * C::WS;
+                return p.ws + (2 * ((long long)(c0 + i) * p.lanes + lane_q) + (i == 0 ? odd : 0)) * C::WS;
             };
             float M = ninf(), lsum = 0.f;
             for (int i0 = 0; i0 < n; i0 += 32) {
@@ -792,10 +800,19 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
     p.wait_limit_ns = kWaitLimitNs;
     p.status = device_status_word();
     if (!p.status) return ATTN_ERR_CUDA;
-    int dev = 0;
+    int dev = 0, n_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&p.n_cta, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || p.n_cta < 1)
+        cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n_sm < 1)
         return ATTN_ERR_CUDA;
+    // As many lanes as divide the pairs evenly and leave at most a tenth of the SMs without
+    // a CTA (8 KV heads: 144 CTAs of 148 SMs).
+    const int q = a.Hkv * p.n_rt;
+    p.lanes = 1;
+    for (int l = 2; l <= q && l <= n_sm; ++l)
+        if (q % l == 0 && n_sm / l * l * 10 >= n_sm * 9) p.lanes = l;
+    p.segs = q / p.lanes;
+    p.n_run = n_sm / p.lanes;
+    const int n_cta = p.lanes * p.n_run;
     CUtensorMap tq, tk, tv;
     attn_status_t st;
     const uint64_t rows = (uint64_t)a.num_blocks * a.block_size;
@@ -806,14 +823,14 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
     if (kernel_setup(reinterpret_cast<const void *>(kernel), C::SMEM, kTreeRegs) != cudaSuccess)
         return ATTN_ERR_CUDA;
     void *ws = nullptr;
-    if (workspace_alloc(&ws, (size_t)2 * p.n_cta * C::WS * sizeof(float), stream) != cudaSuccess)
+    if (workspace_alloc(&ws, (size_t)2 * n_cta * C::WS * sizeof(float), stream) != cudaSuccess)
         return ATTN_ERR_CUDA;
     p.ws = static_cast<float *>(ws);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(n_cta), 1, 1);
     cfg.blockDim = dim3(kTreeThreads, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
@@ -823,7 +840,7 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
     // a row per warp while the blocks fit on the SMs at once, four where that leaves more
     // blocks that only find their segment whole
     const long long fine = ((long long)p.R + 7) / 8 * a.B * a.Hkv;
-    const int rows_per_block = fine <= 8ll * p.n_cta ? 8 : 32;
+    const int rows_per_block = fine <= 8ll * n_cta ? 8 : 32;
     const int row_blocks = (p.R + rows_per_block - 1) / rows_per_block;
     if (st == ATTN_OK) {
         cfg.gridDim = dim3(static_cast<unsigned>(row_blocks) * a.B * a.Hkv, 1, 1);
