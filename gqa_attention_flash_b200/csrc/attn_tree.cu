@@ -86,6 +86,7 @@ static_assert(TreeCfg<128, false>::SMEM <= 232448 && TreeCfg<128, true>::SMEM <=
 struct TreeParams {
     __nv_bfloat16 *O;
     float *ws;
+    long long *before;  // workspace (B + 1): key tiles of one pair before each sequence, all of them
     const int32_t *tables, *ctx, *parents, *drafts;
     int B, Hq, Hkv, T, R, n_rt, max_blocks, num_blocks, shift, box_rows;
     // (KV head, row pass) pair q runs in lane q % lanes, as segment q / lanes of each
@@ -219,6 +220,14 @@ __device__ __forceinline__ bool tree_setup(const TreeParams &p, uint8_t *smem, T
     long long mine = 0, total;
     for (int b = b0; b < b1; ++b) mine += tree_lens(p, b, blockIdx.x == 0).nt;
     const long long before = block_scan(mine, warp_sums, total);
+    if (blockIdx.x == 0) {  // for the combine
+        long long pre = before;
+        for (int b = b0; b < b1; ++b) {
+            p.before[b] = pre;
+            pre += tree_lens(p, b, false).nt;
+        }
+        if (threadIdx.x == 0) p.before[p.B] = total;
+    }
     const long long H = p.segs;
     const long long share = (total * H + p.n_run - 1) / p.n_run;
     w.f_first = w.f = blockIdx.x / p.lanes * share;
@@ -698,22 +707,12 @@ template <int D, class C>
 __global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const TreeParams p, int row_blocks, int rows_per_block) {
     constexpr int PER = D / 32;
-    __shared__ long long warp_sums[kCombineThreads / 32], found;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int rb = static_cast<int>(blockIdx.x % row_blocks);
     const int bh = static_cast<int>(blockIdx.x / row_blocks);
     const int hkv = bh % p.Hkv, b = bh / p.Hkv;
-    const int per = (p.B + kCombineThreads - 1) / kCombineThreads;
-    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    long long mine = 0, total, upto = 0;
-    for (int x = b0; x < b1; ++x) {
-        if (x == b) upto = mine;
-        mine += tree_lens(p, x, false).nt;
-    }
-    const long long before = block_scan(mine, warp_sums, total);
-    if (b >= b0 && b < b1) found = before + upto;
-    __syncthreads();
+    const long long found = p.before[b], total = p.before[p.B];
     const long long H = p.segs;
     const long long share = (total * H + p.n_run - 1) / p.n_run;
     const TreeLens len = tree_lens(p, b, false);
@@ -823,9 +822,11 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
     if (kernel_setup(reinterpret_cast<const void *>(kernel), C::SMEM, kTreeRegs) != cudaSuccess)
         return ATTN_ERR_CUDA;
     void *ws = nullptr;
-    if (workspace_alloc(&ws, (size_t)2 * n_cta * C::WS * sizeof(float), stream) != cudaSuccess)
+    const size_t partials = (size_t)2 * n_cta * C::WS * sizeof(float);  // a multiple of 8
+    if (workspace_alloc(&ws, partials + ((size_t)a.B + 1) * sizeof(long long), stream) != cudaSuccess)
         return ATTN_ERR_CUDA;
     p.ws = static_cast<float *>(ws);
+    p.before = reinterpret_cast<long long *>(static_cast<char *>(ws) + partials);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -185,8 +185,9 @@ attn_status_t attn_fwd_sinks(void *O, const void *Q, const void *K, const void *
 
 /*
  * attn_bwd_sinks -- backward of attn_fwd_sinks: attn_bwd on that mask, with the same
- * arguments, padding rules, workspace and errors (window >= 1, sinks >= 0, as in the
- * forward).
+ * arguments, padding rules and errors (window >= 1, sinks >= 0, as in the forward).  Its
+ * workspace is attn_bwd's, plus fp32 partials where the items of a key tile are split over
+ * CTAs (up to about 40 MB).
  */
 attn_status_t attn_bwd_sinks(void *dQ, void *dK, void *dV, const void *dO, const void *Q,
                              const void *K, const void *V, const void *O, const float *LSE,
@@ -335,11 +336,12 @@ attn_status_t attn_decode_noalloc(void *O, const void *Q, const void *K, const v
  * model with a sliding window and sinks.  The query is the last cached token, position
  * lengths[b] - 1, so it sees the keys
  *   j < lengths[b]  with  j >= lengths[b] - window  or  j < sinks.
- * Cache rows of other keys are not read as values that reach O, whatever they hold; in
- * the paged cache, entries of block_tables for pages without a visible key are not read
- * either (attn_cache_free may have given them back).
+ * Cache rows of other keys never reach O, whatever they hold; in the paged cache, entries
+ * of block_tables for pages without a visible key may hold anything (attn_cache_free
+ * leaves -1 there), and those pages are not read.
  * Arguments and errors as attn_decode / attn_decode_paged; window >= 1, sinks >= 0;
- * n_splits 0..64, 0 = chosen by the library from the sizes.
+ * n_splits 0..64, 0 = chosen by the library from the sizes.  Up to 8 slices need no
+ * workspace.
  */
 attn_status_t attn_decode_sinks(void *O, const void *Q, const void *K, const void *V,
                                 const int32_t *lengths, int window, int sinks, int n_splits,
@@ -372,7 +374,9 @@ attn_status_t attn_decode_paged_sinks(void *O, const void *Q, const void *K_cach
  * each is flagged ATTN_ERR_DEVICE_BOUNDS.  Cache rows at or past context_lens[b] +
  * draft_lens[b] never reach O; those before it must hold finite values.
  *   Sizes: B >= 0; T 0..256; Hq, Hkv >= 1, Hq % Hkv == 0, Hq / Hkv <= 16;
- *          block_size a power of two >= 8; D in {64, 128}.
+ *          max_blocks_per_seq >= 1; block_size a power of two >= 8; D in {64, 128}.
+ * Allocates a stream-ordered workspace (partial results of the sequences that several
+ * SMs share, up to 39 MB, and B + 1 integers).
  */
 attn_status_t attn_tree_paged(void *O, const void *Q, const void *K_cache, const void *V_cache,
                               const int32_t *block_tables, const int32_t *context_lens,
