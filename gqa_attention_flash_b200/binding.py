@@ -138,6 +138,20 @@ def _same_device(**tensors):
                              f"cuda:{cur}")
 
 
+def _on_device(names, *tensors):
+    """_same_device for tensors whose names stand in ``names`` (in order, separated by
+    spaces), without building a dict on every call; returns the device's index."""
+    cur = None
+    for t in tensors:
+        if t is not None:
+            idx = t.get_device()
+            if idx != cur:
+                if cur is not None or idx < 0 or idx != torch.cuda.current_device():
+                    _same_device(**dict(zip(names.split(), tensors)))  # raises
+                cur = idx
+    return cur
+
+
 def _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths):
     B, Hq, Sq, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 4)
     _, Hkv, Sk, _ = _tensor(K, "K", torch.bfloat16, (B, None, None, D))
@@ -157,11 +171,11 @@ def _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -297,7 +311,7 @@ def _check_decode(O, Q, K, V, lengths):
     _tensor(V, "V", torch.bfloat16, (B, Hkv, S_cap, D))
     _tensor(O, "O", torch.bfloat16, (B, Hq, D))
     _tensor(lengths, "lengths", torch.int32, (B,))
-    _same_device(O=O, Q=Q, K=K, V=V, lengths=lengths)
+    _on_device("O Q K V lengths", O, Q, K, V, lengths)
     return B, Hq, Hkv, S_cap, D
 
 
@@ -342,10 +356,10 @@ def attn_fwd_sinks(O, Q, K, V, LSE, scale, window, sinks, input_pos=0, k_lengths
     """attn_fwd, causal, with a sliding window and the first ``sinks`` keys always visible:
     query position p sees keys j <= p with j > p - window or j < sinks."""
     B, Hq, Hkv, Sq, Sk, D = _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths)
-    _same_device(O=O, Q=Q, K=K, V=V, LSE=LSE, k_lengths=k_lengths, q_lengths=q_lengths)
+    dev = _on_device("O Q K V LSE k_lengths q_lengths", O, Q, K, V, LSE, k_lengths, q_lengths)
     rc = lib.attn_fwd_sinks(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D,
                             float(scale), int(window), int(sinks), int(input_pos),
-                            _ptr(k_lengths), _ptr(q_lengths), _stream(stream))
+                            _ptr(k_lengths), _ptr(q_lengths), _stream(stream, dev))
     _check(rc, "attn_fwd_sinks")
 
 
@@ -378,11 +392,11 @@ def attn_decode_paged_sinks(O, Q, K_cache, V_cache, block_tables, seq_lens, wind
     _tensor(O, "O", torch.bfloat16, (B, Hq, D))
     num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
     _tensor(seq_lens, "seq_lens", torch.int32, (B,))
-    _same_device(O=O, Q=Q, K_cache=K_cache, V_cache=V_cache, block_tables=block_tables,
-                 seq_lens=seq_lens)
+    dev = _on_device("O Q K_cache V_cache block_tables seq_lens",
+                     O, Q, K_cache, V_cache, block_tables, seq_lens)
     rc = lib.attn_decode_paged_sinks(_ptr(O), _ptr(Q), _ptr(K_cache), _ptr(V_cache),
                                      _ptr(block_tables), _ptr(seq_lens), int(window), int(sinks),
-                                     int(n_splits), _stream(stream), B, Hq, Hkv, num_blocks,
+                                     int(n_splits), _stream(stream, dev), B, Hq, Hkv, num_blocks,
                                      block_size, max_blocks, D)
     _check(rc, "attn_decode_paged_sinks")
 
@@ -399,10 +413,11 @@ def attn_tree_paged(O, Q, K_cache, V_cache, block_tables, context_lens, parents,
     _tensor(parents, "parents", torch.int32, (B, T))
     if draft_lens is not None:
         _tensor(draft_lens, "draft_lens", torch.int32, (B,))
-    _same_device(O=O, Q=Q, K_cache=K_cache, V_cache=V_cache, block_tables=block_tables,
-                 context_lens=context_lens, parents=parents, draft_lens=draft_lens)
+    dev = _on_device("O Q K_cache V_cache block_tables context_lens parents draft_lens",
+                     O, Q, K_cache, V_cache, block_tables, context_lens, parents, draft_lens)
     rc = lib.attn_tree_paged(_ptr(O), _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(block_tables),
-                             _ptr(context_lens), _ptr(parents), _ptr(draft_lens), _stream(stream),
+                             _ptr(context_lens), _ptr(parents), _ptr(draft_lens),
+                             _stream(stream, dev),
                              B, Hq, Hkv, T, num_blocks, block_size, max_blocks, D)
     _check(rc, "attn_tree_paged")
 
@@ -426,10 +441,11 @@ def cache_append(K_cache, V_cache, K_new, V_new, block_tables, start, n_new=None
     _tensor(start, "start", torch.int32, (B,))
     if n_new is not None:
         _tensor(n_new, "n_new", torch.int32, (B,))
-    _same_device(K_cache=K_cache, V_cache=V_cache, K_new=K_new, V_new=V_new,
-                 block_tables=block_tables, start=start, n_new=n_new)
+    dev = _on_device("K_cache V_cache K_new V_new block_tables start n_new",
+                     K_cache, V_cache, K_new, V_new, block_tables, start, n_new)
     rc = lib.attn_cache_append(_ptr(K_cache), _ptr(V_cache), _ptr(K_new), _ptr(V_new),
-                               _ptr(block_tables), _ptr(start), _ptr(n_new), _stream(stream), B,
+                               _ptr(block_tables), _ptr(start), _ptr(n_new),
+                               _stream(stream, dev), B,
                                Hkv, T, num_blocks, block_size, max_blocks, D)
     _check(rc, "attn_cache_append")
 
@@ -443,10 +459,11 @@ def cache_compact(K_cache, V_cache, block_tables, base, keep, n_keep=None, strea
     _tensor(base, "base", torch.int32, (B,))
     if n_keep is not None:
         _tensor(n_keep, "n_keep", torch.int32, (B,))
-    _same_device(K_cache=K_cache, V_cache=V_cache, block_tables=block_tables, base=base, keep=keep,
-                 n_keep=n_keep)
+    dev = _on_device("K_cache V_cache block_tables base keep n_keep",
+                     K_cache, V_cache, block_tables, base, keep, n_keep)
     rc = lib.attn_cache_compact(_ptr(K_cache), _ptr(V_cache), _ptr(block_tables), _ptr(base),
-                                _ptr(keep), _ptr(n_keep), _stream(stream), B, Hkv, A, num_blocks,
+                                _ptr(keep), _ptr(n_keep),
+                                _stream(stream, dev), B, Hkv, A, num_blocks,
                                 block_size, max_blocks, D)
     _check(rc, "attn_cache_compact")
 
@@ -457,9 +474,9 @@ def cache_copy_blocks(K_cache, V_cache, src, dst, stream=None):
     _tensor(V_cache, "V_cache", torch.bfloat16, (num_blocks, block_size, Hkv, D))
     (N,) = _tensor(src, "src", torch.int32, (None,))
     _tensor(dst, "dst", torch.int32, (N,))
-    _same_device(K_cache=K_cache, V_cache=V_cache, src=src, dst=dst)
+    dev = _on_device("K_cache V_cache src dst", K_cache, V_cache, src, dst)
     rc = lib.attn_cache_copy_blocks(_ptr(K_cache), _ptr(V_cache), _ptr(src), _ptr(dst),
-                                    _stream(stream), N, num_blocks, block_size, Hkv, D)
+                                    _stream(stream, dev), N, num_blocks, block_size, Hkv, D)
     _check(rc, "attn_cache_copy_blocks")
 
 
@@ -479,10 +496,11 @@ def cache_fork(block_tables, ref_counts, seq_lens, parents, children, copy_src, 
     _tensor(children, "children", torch.int32, (N,))
     _tensor(copy_src, "copy_src", torch.int32, (N,))
     _tensor(copy_dst, "copy_dst", torch.int32, (N,))
-    _same_device(block_tables=block_tables, ref_counts=ref_counts, seq_lens=seq_lens,
-                 parents=parents, children=children, copy_src=copy_src, copy_dst=copy_dst)
+    dev = _on_device("block_tables ref_counts seq_lens parents children copy_src copy_dst",
+                     block_tables, ref_counts, seq_lens, parents, children, copy_src, copy_dst)
     rc = lib.attn_cache_fork(_ptr(block_tables), _ptr(ref_counts), _ptr(seq_lens), _ptr(parents),
-                             _ptr(children), _ptr(copy_src), _ptr(copy_dst), _stream(stream), N, R,
+                             _ptr(children), _ptr(copy_src), _ptr(copy_dst),
+                             _stream(stream, dev), N, R,
                              num_blocks, int(block_size), max_blocks)
     _check(rc, "attn_cache_fork")
 
@@ -493,10 +511,10 @@ def cache_extend(block_tables, ref_counts, from_lens, to_lens, block_size, strea
     R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
     _tensor(from_lens, "from_lens", torch.int32, (R,))
     _tensor(to_lens, "to_lens", torch.int32, (R,))
-    _same_device(block_tables=block_tables, ref_counts=ref_counts, from_lens=from_lens,
-                 to_lens=to_lens)
+    dev = _on_device("block_tables ref_counts from_lens to_lens",
+                     block_tables, ref_counts, from_lens, to_lens)
     rc = lib.attn_cache_extend(_ptr(block_tables), _ptr(ref_counts), _ptr(from_lens), _ptr(to_lens),
-                               _stream(stream), R, num_blocks, int(block_size), max_blocks)
+                               _stream(stream, dev), R, num_blocks, int(block_size), max_blocks)
     _check(rc, "attn_cache_extend")
 
 
@@ -506,10 +524,10 @@ def cache_free(block_tables, ref_counts, rows, first, last, stream=None):
     (N,) = _tensor(rows, "rows", torch.int32, (None,))
     _tensor(first, "first", torch.int32, (N,))
     _tensor(last, "last", torch.int32, (N,))
-    _same_device(block_tables=block_tables, ref_counts=ref_counts, rows=rows, first=first,
-                 last=last)
+    dev = _on_device("block_tables ref_counts rows first last",
+                     block_tables, ref_counts, rows, first, last)
     rc = lib.attn_cache_free(_ptr(block_tables), _ptr(ref_counts), _ptr(rows), _ptr(first),
-                             _ptr(last), _stream(stream), N, R, num_blocks, max_blocks)
+                             _ptr(last), _stream(stream, dev), N, R, num_blocks, max_blocks)
     _check(rc, "attn_cache_free")
 
 

@@ -1019,7 +1019,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
         // Items (query head, query tile) of a tile with sinks and of another one, lengths
         // aside.  A CTA of more items than an SM's share (and than 4: a partial costs about
         // as much as one item) is split; tiles without sinks only where there are fewer than
-        // SMs (B2 Hq8 S1000 w200 D64: 58 -> 27 us a call).
+        // SMs (B2 Hq8 S1000 w200 D64: 59 -> 31 us).
         const long long sink_keys = a.sinks < a.Sk ? a.sinks : a.Sk;
         p.sink_tiles = static_cast<int>((sink_keys + TB - 1) / TB);
         const long long n_s = (long long)p.group * n_qt;
