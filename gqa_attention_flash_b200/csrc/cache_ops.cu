@@ -153,15 +153,27 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
     }
     if (n <= 0) return;
     // The whole list is checked first: ascending, inside the table, on pages of the pool.
+    // Four entries per thread and step, so that their lookups overlap.
     bool bad = base < 0;
-    for (int k = threadIdx.x; k < n && !bad; k += kCompactThreads) {
-        const int x = keep[k];
-        const int before = k > 0 ? keep[k - 1] : -1;
-        bad = x <= before || x < 0 || base + x >= p.capacity;
-        if (!bad) {
-            const long long from = pool_row(bt, static_cast<int>(base + x), p.shift, p.num_blocks);
-            const long long to = pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks);
-            bad = from < 0 || to < 0;
+    for (int k0 = threadIdx.x; k0 < n; k0 += 4 * kCompactThreads) {
+        int x[4], before[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = k0 + i * kCompactThreads;
+            x[i] = k < n ? keep[k] : 0;
+            before[i] = k < n && k > 0 ? keep[k - 1] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = k0 + i * kCompactThreads;
+            if (k >= n) continue;
+            // (an entry that passes has k <= x, so both positions lie in the table)
+            const bool fits = base >= 0 && x[i] > before[i] && x[i] >= k && base + x[i] < p.capacity;
+            const long long from =
+                fits ? pool_row(bt, static_cast<int>(base + x[i]), p.shift, p.num_blocks) : -1;
+            const long long to =
+                fits ? pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks) : -1;
+            bad = bad || from < 0 || to < 0;
             if (k < kCompactList) {
                 rows_from[k] = static_cast<int>(from);
                 rows_to[k] = static_cast<int>(to);
