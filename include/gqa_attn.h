@@ -176,7 +176,9 @@ attn_status_t attn_bwd(void *dQ, void *dK, void *dV, const void *dO, const void 
  *
  * Arguments, outputs and errors as attn_fwd_varlen with causal = 1, except that
  * window >= 1 is required and sinks >= 0 is added.  sinks = 0 is attn_fwd_varlen with
- * that window; a window of input_pos + Sq or more is plain causal attention.
+ * that window; a window of input_pos + Sq or more is plain causal attention.  Rows of V
+ * below k_lengths[b] must hold finite values, also those that no query of the call sees:
+ * they may enter products with weight zero.
  */
 attn_status_t attn_fwd_sinks(void *O, const void *Q, const void *K, const void *V, float *LSE,
                              int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
