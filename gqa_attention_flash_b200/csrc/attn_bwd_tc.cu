@@ -183,11 +183,12 @@ __device__ __forceinline__ void mma_kmajor(uint32_t d_tmem, uint32_t a_smem, uin
 // packs over its own fp32 columns); otherwise K pairs are contiguous.
 template <int D, bool kSplit>
 __device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem,
-                                           bool accumulate) {
+                                           bool accumulate, int steps = TB / 16) {
     using C = TcCfg<D>;
     constexpr uint32_t id = idesc_bf16_f32(TB, D, 0, 1);
 #pragma unroll
     for (int kk = 0; kk < TB / 16; ++kk) {
+        if (kk >= steps) break;
         const uint32_t a_col = kSplit ? (kk >> 2) * 64 + (kk & 3) * 8 : kk * 8;
         mma_ts(d_tmem, a_tmem + a_col, smem_desc_sw128(b_smem + kk * 16 * 128, C::BOX, 1024), id,
                (accumulate || kk > 0) ? 1u : 0u);
@@ -247,6 +248,11 @@ __device__ __forceinline__ void tc_teardown(uint8_t *smem, uint32_t tmem) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// What rounding two values to bf16 (`packed`) left of them, rounded to bf16 too.
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t packed) {
+    return pack_bf16x2(a - __uint_as_float(packed << 16), b - __uint_as_float(packed & 0xffff0000u));
 }
 
 // Write columns [c0, c0 + D/2) of this thread's TMEM lane of an fp32 accumulator,
@@ -690,6 +696,13 @@ __global__ void __launch_bounds__(256) bwd_dkdv_reduce_kernel(const TcParams p) 
 // ---------------------------------------------------------------------------------
 // dQ of one 128-row query tile
 // ---------------------------------------------------------------------------------
+// P and dS are rounded to bf16 for their products, as P is in the forward.  kSink: the sinks
+// hold most of a row's weight and their keys have a direction in common, in which a row's dS
+// sums to zero, so their roundings would be most of dQ's error (2.7e-3 of fp64, 2-norm,
+// against 1.7e-3 for rounding the result alone).  On the columns of the sinks dS therefore
+// enters as two bf16 terms, the second in columns of the score that are free by then: one
+// more K-step per 16 sinks on their tile (2.3e-3; B4 S4096 w1024: 1130 -> 1150 us).
+//
 // Shared memory of the dQ kernel: Q and dO resident, three K slots and two V
 // slots (K of a tile is read last, by dQ += dS K, and first, by the next-but-one
 // S, so it gets the deeper ring).
@@ -837,6 +850,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 tc_fence_after();
                 mma_tmem_a<D, true>(tmem + C::COL_DQ, tmem + C::COL_S + (g & 1) * TB,
                                     sbase + C::k_slot(g % C::NK), g > 0);  // dQ += dS K
+                if (const int n = p.sinks - key_tile(g) * TB; kSink && n > 0)  // its second term
+                    mma_tmem_a<D, true>(tmem + C::COL_DQ, tmem + C::COL_S + (g & 1) * TB + 32,
+                                        sbase + C::k_slot(g % C::NK), true, (min(n, TB) + 15) / 16);
                 mma_commit(bar(C::BAR_EMPTYK + g % C::NK));
                 if (g + 1 < n_kt && !(ok = issue_dp(g + 1))) break;
                 if (g + 2 < n_kt && !(ok = issue_s(g + 2))) break;
@@ -910,18 +926,30 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 for (int c = 0; c < 2; ++c) {
                     uint32_t pk[16];
                     const uint64_t nd2 = f2_pack(-del, -del);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
+                    auto ds = [&](int k, float &d0, float &d1) {  // dS of columns 32 c + 2 k, + 1
                         const int x = 32 * c + 2 * k;
-                        float d0, d1;
                         f2_unpack(f2_mul(f2_pack(pr[x], pr[x + 1]),
                                          f2_add(f2_pack(__uint_as_float(dv[c][2 * k]),
                                                         __uint_as_float(dv[c][2 * k + 1])),
                                                 nd2)),
                                   d0, d1);
+                    };
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float d0, d1;
+                        ds(k, d0, d1);
                         pk[k] = pack_bf16x2(d0, d1);
                     }
                     tmem_st16(t_s + 16 * c, pk);  // dS over this warp's own S columns
+                    if (kSink && 32 * c < cs) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float d0, d1;
+                            ds(k, d0, d1);
+                            pk[k] = pack_rest(d0, d1, pk[k]);
+                        }
+                        tmem_st16(t_s + 32 + 16 * c, pk);
+                    }
                 }
             }
             tmem_wait_st();
