@@ -97,7 +97,8 @@ def compact_ref(pool, t, base, keep, block):
 
 @pytest.mark.parametrize("B,Hkv,D,block,span,share", [
     (1, 1, 64, 8, 1, 1.0), (1, 8, 128, 16, 8, 0.5), (3, 2, 64, 8, 60, 0.3), (2, 3, 128, 64, 500, 0.9),
-    (2, 1, 64, 16, 2000, 0.5), (1, 2, 128, 32, 700, 1.0), (4, 8, 128, 16, 129, 0.02)])
+    (2, 1, 64, 16, 2000, 0.5), (1, 2, 128, 32, 700, 1.0), (4, 8, 128, 16, 129, 0.02),
+    (2, 1, 64, 16, 7000, 0.9), (1, 3, 64, 8, 4097, 0.5001), (1, 1, 128, 4096, 9000, 0.3)])
 def test_compact(B, Hkv, D, block, span, share):
     g = torch.Generator().manual_seed(span)
     base = [int(torch.randint(0, 40, (1,), generator=g)) for _ in range(B)]
@@ -325,6 +326,29 @@ def test_fork_refuses_pairs_that_meet():
         ws, wd, _ = m.fork(par2, chi)
         m.same(t, refs, L)
         assert src.tolist() == ws and dst.tolist() == wd
+
+
+def test_fork_many_pairs_from_few_parents():
+    """1500 children of three parents in one call, in an order of their own; the pool runs out
+    before the last of them."""
+    R, block, n = 1503, 8, 1300
+    lens = [21, 16, 5] + [0] * 1500
+    m = Model([[0, 1, 2], [3, 4, -1], [5, -1, -1]] + [[-1] * 3] * 1500, n, block, lens)
+    t, refs, L = i32(m.t), i32(m.refs), i32(m.lens)
+    g = torch.Generator().manual_seed(4)
+    par = torch.randint(0, 3, (1500,), generator=g).tolist()
+    chi = (3 + torch.randperm(1500, generator=g)).tolist()
+    for k in (5, 700, 1499):
+        par[k] = 2  # parents with a part-filled page first, in the middle and last
+    src, dst = (torch.full((1500,), 9, dtype=torch.int32, device="cuda") for _ in range(2))
+    for r in range(3, 1200):  # most of the pool is taken
+        m.refs[r + 3] = 1
+    refs = i32(m.refs)
+    binding.cache_fork(t, refs, L, i32(par), i32(chi), src, dst, block)
+    ws, wd, ok = m.fork(par, chi)
+    assert not ok and status() == "ATTN_ERR_NO_PAGES"
+    m.same(t, refs, L)
+    assert src.tolist() == ws and dst.tolist() == wd
 
 
 def test_extend_keeps_freed_window_pages_empty():

@@ -6,7 +6,7 @@ value: the kernels round each weight p (forward, dV) or p (dP - delta) (dQ, dK) 
 before its product, and the result once more, so
     |dO| <= u (sum_j p_j |v_j| + |O|),  |d dV| <= u (sum_i p_i |dO_i| + |dV|),
     |d dQ| <= u (scale sum_j |dS_j| |k_j| + |dQ|), and dK likewise.
-Everything else is fp32: sums of n <= 2^10 terms lose at most n 2^-24 = 2^-14 of the sum
+Everything else is fp32: sums of n <= 2^11 terms lose at most n 2^-24 = 2^-13 of the sum
 of their magnitudes, which the bounds add with the magnitudes before any cancellation."""
 import math
 
@@ -19,7 +19,7 @@ from gqa_attention_flash_b200 import workloads as W
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -8
-F32 = 2.0 ** -14
+F32 = 2.0 ** -13
 NEG = float("-inf")
 BF = torch.bfloat16
 
@@ -79,6 +79,8 @@ CASES = [
     (2, 32, 2, 260, 0, 128, 33, 4, None, None),
     (1, 3, 3, 1030, 0, 64, 127, 128, None, None),
     (1, 2, 1, 512, 0, 128, 128, 128, None, None),
+    (1, 32, 1, 1300, 0, 64, 64, 4, None, None),        # a sink tile of many items, split
+    (4, 16, 8, 900, 0, 128, 250, 4, (900, 899, 1, 450), (900, 899, 1, 450)),
 ]
 
 
@@ -216,6 +218,10 @@ DECODE = [
     (2, 4, 4, 64, 0, [1000, 640], 100, 1, 0, 64),
     (2, 8, 1, 128, 0, [2048, 257], 130, 33, 0, 256),
     (2, 10, 2, 128, 0, [900, 333], 2 ** 31 - 1, 2 ** 31 - 1, 0, 32),
+    (2, 16, 1, 128, 1500, [1500, 40], 700, 9, 8, 0),
+    (3, 32, 2, 128, 0, [1500, 64, 700], 640, 65, 6, 16),
+    (1, 4, 2, 64, 0, [5000], 300, 4, 9, 4096),
+    (40, 8, 8, 64, 0, [17 * k for k in range(40)], 100, 4, 0, 8),
 ]
 
 

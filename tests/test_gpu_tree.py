@@ -98,6 +98,10 @@ CASES = [
     (1, 16, 1, 128, 100, [90], [99], 128, "random"),        # 1600 rows of one KV head
     (2, 6, 2, 128, 3, [2900, 2048], [3, 2], 512, "star"),
     (1, 10, 2, 128, 26, [60], [26], 16, "random"),          # 130 rows: one past a tile
+    (2, 5, 5, 64, 9, [4500, 100], [9, 2], 4096, "random"),  # pages of many tiles
+    (1, 64, 64, 64, 2, [300], [2], 8, "star"),              # more KV heads than lanes divide evenly
+    (1, 37, 37, 128, 3, [130], [3], 16, "binary"),
+    (1, 150, 150, 64, 1, [20], [1], 16, "chain"),
     (8, 4, 1, 64, 4, [0, 5, 64, 128, 129, 700, 1500, 2], [4, 4, 4, 0, 1, 4, 4, 4], 16, "random"),
 ]
 
