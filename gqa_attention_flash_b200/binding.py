@@ -100,20 +100,24 @@ def _ptr(t):
 # float16 tensor or a tensor on another device from the layout it expects.  The
 # wrappers therefore refuse such tensors here, before any call into the library.
 def _tensor(t, name, dtype, shape):
-    """Check dtype, shape (entries of None are free) and row-major contiguity;
-    returns the shape."""
+    """Check dtype, shape (entries of None are free; a number: that many free entries) and
+    row-major contiguity; returns the shape."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     got = t.shape
     if got != shape:  # a torch.Size is a tuple; look at the free entries only then
-        ok = len(got) == len(shape)
-        if ok:
-            for g, w in zip(got, shape):
-                if w is not None and w != g:
-                    ok = False
+        if type(shape) is int:
+            ok = len(got) == shape
+        else:
+            ok = len(got) == len(shape)
+            if ok:
+                for g, w in zip(got, shape):
+                    if w is not None and w != g:
+                        ok = False
         if not ok:
+            shape = (None,) * shape if type(shape) is int else shape
             want = "(" + ", ".join("*" if w is None else str(w) for w in shape) + ")"
             raise ValueError(f"{name} has shape {tuple(got)}, expected {want}")
     if not t.is_contiguous():
@@ -153,7 +157,7 @@ def _on_device(names, *tensors):
 
 
 def _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths):
-    B, Hq, Sq, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 4)
+    B, Hq, Sq, D = _tensor(Q, "Q", torch.bfloat16, 4)
     _, Hkv, Sk, _ = _tensor(K, "K", torch.bfloat16, (B, None, None, D))
     _tensor(V, "V", torch.bfloat16, (B, Hkv, Sk, D))
     _tensor(O, "O", torch.bfloat16, (B, Hq, Sq, D))
@@ -240,7 +244,7 @@ def rbs_block_mask(Q, K, alpha_base=0.22, alpha_rescue=0.18, diagonal=1, want_sc
                    stream=None):
     """Block-sparse prefill mask from the RBS block scores: uint8 (B, Hq, nqb, nkb)
     device tensor (2 = keep, 0 = skip), plus the (base, rescue) scores if asked."""
-    B, Hq, Sq, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 4)
+    B, Hq, Sq, D = _tensor(Q, "Q", torch.bfloat16, 4)
     _, Hkv, Sk, _ = _tensor(K, "K", torch.bfloat16, (B, None, None, D))
     _same_device(Q=Q, K=K)
     shape = (B, Hq, (Sq + 63) // 64, (Sk + 63) // 64)
@@ -306,7 +310,7 @@ def block_mask_build(Sq, Sk, keep, input_pos=0):
 
 
 def _check_decode(O, Q, K, V, lengths):
-    B, Hq, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 3)
+    B, Hq, D = _tensor(Q, "Q", torch.bfloat16, 3)
     _, Hkv, S_cap, _ = _tensor(K, "K", torch.bfloat16, (B, None, None, D))
     _tensor(V, "V", torch.bfloat16, (B, Hkv, S_cap, D))
     _tensor(O, "O", torch.bfloat16, (B, Hq, D))
@@ -326,7 +330,7 @@ def attn_decode(O, Q, K, V, lengths, n_splits=8, stream=None):
 def attn_decode_paged(O, Q, K_cache, V_cache, block_tables, seq_lens, n_splits=8, stream=None):
     """Decode from a paged cache: Q (B,Hq,D); K/V caches (num_blocks, block_size, Hkv, D);
     block_tables int32 (B, max_blocks); seq_lens int32 (B,); O (B,Hq,D) filled in place."""
-    B, Hq, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 3)
+    B, Hq, D = _tensor(Q, "Q", torch.bfloat16, 3)
     num_blocks, block_size, Hkv, _ = _tensor(K_cache, "K_cache", torch.bfloat16,
                                              (None, None, None, D))
     _tensor(V_cache, "V_cache", torch.bfloat16, (num_blocks, block_size, Hkv, D))
@@ -388,7 +392,7 @@ def attn_decode_paged_sinks(O, Q, K_cache, V_cache, block_tables, seq_lens, wind
                             n_splits=0, stream=None):
     """attn_decode_sinks from a paged cache; table entries of pages without a visible key
     are not read."""
-    B, Hq, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 3)
+    B, Hq, D = _tensor(Q, "Q", torch.bfloat16, 3)
     _tensor(O, "O", torch.bfloat16, (B, Hq, D))
     num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
     _tensor(seq_lens, "seq_lens", torch.int32, (B,))
@@ -406,7 +410,7 @@ def attn_tree_paged(O, Q, K_cache, V_cache, block_tables, context_lens, parents,
     """Attention of T drafted tokens per sequence: Q, O (B,Hq,T,D); draft i stands at cache
     position context_lens[b] + i, continues draft parents[b][i] (-1: the context) and sees the
     context, itself and its ancestors.  Rows past draft_lens[b] (int32 (B,), or None = T) get 0."""
-    B, Hq, T, D = _tensor(Q, "Q", torch.bfloat16, (None,) * 4)
+    B, Hq, T, D = _tensor(Q, "Q", torch.bfloat16, 4)
     _tensor(O, "O", torch.bfloat16, (B, Hq, T, D))
     num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
     _tensor(context_lens, "context_lens", torch.int32, (B,))
@@ -433,7 +437,7 @@ def _check_pool(K_cache, V_cache, block_tables, B, D):
 def cache_append(K_cache, V_cache, K_new, V_new, block_tables, start, n_new=None, stream=None):
     """Write K_new, V_new (B,Hkv,T,D) to positions start[b] + t of each sequence's pages, for
     t < n_new[b] (int32 (B,), or None = T)."""
-    B, Hkv, T, D = _tensor(K_new, "K_new", torch.bfloat16, (None,) * 4)
+    B, Hkv, T, D = _tensor(K_new, "K_new", torch.bfloat16, 4)
     _tensor(V_new, "V_new", torch.bfloat16, (B, Hkv, T, D))
     num_blocks, block_size, heads, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
     if heads != Hkv:
@@ -453,7 +457,7 @@ def cache_append(K_cache, V_cache, K_new, V_new, block_tables, start, n_new=None
 def cache_compact(K_cache, V_cache, block_tables, base, keep, n_keep=None, stream=None):
     """In place: position base[b] + k of each sequence takes the row of position
     base[b] + keep[b][k], for k < n_keep[b]; keep int32 (B,A) is increasing."""
-    B, A = _tensor(keep, "keep", torch.int32, (None, None))
+    B, A = _tensor(keep, "keep", torch.int32, 2)
     D = K_cache.shape[-1] if isinstance(K_cache, torch.Tensor) and K_cache.dim() else None
     num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
     _tensor(base, "base", torch.int32, (B,))
@@ -470,9 +474,9 @@ def cache_compact(K_cache, V_cache, block_tables, base, keep, n_keep=None, strea
 
 def cache_copy_blocks(K_cache, V_cache, src, dst, stream=None):
     """Page dst[i] takes the contents of page src[i] (int32 (N,), negative = no pair)."""
-    num_blocks, block_size, Hkv, D = _tensor(K_cache, "K_cache", torch.bfloat16, (None,) * 4)
+    num_blocks, block_size, Hkv, D = _tensor(K_cache, "K_cache", torch.bfloat16, 4)
     _tensor(V_cache, "V_cache", torch.bfloat16, (num_blocks, block_size, Hkv, D))
-    (N,) = _tensor(src, "src", torch.int32, (None,))
+    (N,) = _tensor(src, "src", torch.int32, 1)
     _tensor(dst, "dst", torch.int32, (N,))
     dev = _on_device("K_cache V_cache src dst", K_cache, V_cache, src, dst)
     rc = lib.attn_cache_copy_blocks(_ptr(K_cache), _ptr(V_cache), _ptr(src), _ptr(dst),
@@ -481,8 +485,8 @@ def cache_copy_blocks(K_cache, V_cache, src, dst, stream=None):
 
 
 def _check_table(block_tables, ref_counts):
-    R, max_blocks = _tensor(block_tables, "block_tables", torch.int32, (None, None))
-    (num_blocks,) = _tensor(ref_counts, "ref_counts", torch.int32, (None,))
+    R, max_blocks = _tensor(block_tables, "block_tables", torch.int32, 2)
+    (num_blocks,) = _tensor(ref_counts, "ref_counts", torch.int32, 1)
     return R, max_blocks, num_blocks
 
 
@@ -492,7 +496,7 @@ def cache_fork(block_tables, ref_counts, seq_lens, parents, children, copy_src, 
     part-filled one, whose copy is left to cache_copy_blocks(copy_src, copy_dst)."""
     R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
     _tensor(seq_lens, "seq_lens", torch.int32, (R,))
-    (N,) = _tensor(parents, "parents", torch.int32, (None,))
+    (N,) = _tensor(parents, "parents", torch.int32, 1)
     _tensor(children, "children", torch.int32, (N,))
     _tensor(copy_src, "copy_src", torch.int32, (N,))
     _tensor(copy_dst, "copy_dst", torch.int32, (N,))
@@ -521,7 +525,7 @@ def cache_extend(block_tables, ref_counts, from_lens, to_lens, block_size, strea
 def cache_free(block_tables, ref_counts, rows, first, last, stream=None):
     """Give back table entries first[n] .. last[n]-1 of row rows[n] (int32 (N,))."""
     R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
-    (N,) = _tensor(rows, "rows", torch.int32, (None,))
+    (N,) = _tensor(rows, "rows", torch.int32, 1)
     _tensor(first, "first", torch.int32, (N,))
     _tensor(last, "last", torch.int32, (N,))
     dev = _on_device("block_tables ref_counts rows first last",
