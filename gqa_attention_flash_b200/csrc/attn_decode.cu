@@ -280,8 +280,10 @@ __global__ void __launch_bounds__(kDecThreads)
 #pragma unroll
                         for (int k = 0; k < kMaxChunks; ++k) cur[k] = ids[k];
                         if (it + 1 < n_tiles) load_ids(it + 1);
+                        // only the sinks' and the window's edge tiles leave chunks out
+                        const bool edge = kSink && row < vis.win_lo && row + TN > vis.sinks;
                         int n_read = n_chunks;
-                        if constexpr (kSink) {
+                        if (edge) {
                             n_read = 0;
                             for (int k = 0; k < n_chunks; ++k) n_read += vis.any(row + k * br, br) ? 1 : 0;
                         }
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kDecThreads)
                         for (int k = 0; k < kMaxChunks; ++k) {
                             if (k >= n_chunks) break;
                             const int j = row + k * br;
-                            if (kSink && !vis.any(j, br)) continue;
+                            if (edge && !vis.any(j, br)) continue;
                             const int blk = cur[k];
                             if (blk < 0 || blk >= p.num_blocks) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
                             // an out-of-range block reads as zeros (outside the tensor map)
@@ -349,6 +351,8 @@ __global__ void __launch_bounds__(kDecThreads)
                 }
                 const int key0 = tile_row(it) + warp * 16;  // first key of this warp
                 const int key_end = kSink ? len : k1;
+                // some of the warp's 16 keys lie between the sinks and the window
+                const bool cut = kSink && key0 < vis.win_lo && key0 + 16 > vis.sinks;
                 if (key0 < key_end) {
                     const uint32_t kb = sbase + C::OFF_K + st * C::TILE;
                     const uint32_t vb = sbase + C::OFF_V + st * C::TILE;
@@ -366,16 +370,26 @@ __global__ void __launch_bounds__(kDecThreads)
                     }
                     // ---- mask keys past the slice end; online softmax (exp2 domain) ----
                     float mt[2] = {neg_inf(), neg_inf()};
+                    if (kSink && !cut && key0 + 16 <= key_end) {  // all of the warp's keys count
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb)
+                        for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + nb * 8 + 2 * t + (e & 1);
-                            const bool seen = key < key_end && (!kSink || vis.sees(key));
-                            const float x = seen ? sc[nb][e] * p.scale_log2 : neg_inf();
-                            sc[nb][e] = x;
-                            mt[e >> 1] = fmaxf(mt[e >> 1], x);
-                        }
+                            for (int e = 0; e < 4; ++e) {
+                                sc[nb][e] *= p.scale_log2;
+                                mt[e >> 1] = fmaxf(mt[e >> 1], sc[nb][e]);
+                            }
+                    } else {
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = key0 + nb * 8 + 2 * t + (e & 1);
+                                const bool seen = key < key_end && (!kSink || vis.sees(key));
+                                const float x = seen ? sc[nb][e] * p.scale_log2 : neg_inf();
+                                sc[nb][e] = x;
+                                mt[e >> 1] = fmaxf(mt[e >> 1], x);
+                            }
+                    }
                     float alpha[2], m_use[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -410,13 +424,12 @@ __global__ void __launch_bounds__(kDecThreads)
                     // Cache rows at or past the sequence length may hold anything; their
                     // weights are 0, but 0 * NaN is NaN, so zero this warp's such V rows.
                     // With a window, neither do the rows between the sinks and the window.
-                    const bool cut = kSink && key0 < vis.win_lo && key0 + 16 > vis.sinks;
                     const bool tail = (key0 + 16 > len && key0 < p.S_cap) || cut;
                     if (tail) {
                         const int rows_from = max(len - key0, 0);
                         for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
                             const int rrow = idx / (D / 8), ch = idx % (D / 8);
-                            if (rrow >= rows_from || (kSink && !vis.sees(key0 + rrow)))
+                            if (rrow >= rows_from || (cut && !vis.sees(key0 + rrow)))
                                 *reinterpret_cast<uint4 *>(smem + C::OFF_V + st * C::TILE +
                                                            swz_t<kWide>(warp * 16 + rrow, ch)) =
                                     make_uint4(0, 0, 0, 0);
@@ -480,7 +493,9 @@ __global__ void __launch_bounds__(kDecThreads)
                         acc += wt * mo[(w * kMaxGroup + h) * D + d];
                         lsum += wt * ml[w * kMaxGroup + h];
                     }
-                    if constexpr (kCluster) {
+                    if (kCluster && p.n_splits == 1) {  // the only slice: the output itself
+                        p.O[(long long)(b * p.Hq + h0) * D + idx] = __float2bfloat16_rn(acc / lsum);
+                    } else if constexpr (kCluster) {
                         part[idx] = acc / lsum;
                         if (d == 0) part[G * D + h] = M + __log2f(lsum);  // log2 units
                     } else {
@@ -503,6 +518,8 @@ __global__ void __launch_bounds__(kDecThreads)
         __syncthreads();
     }
     if constexpr (kCluster) {
+        // one slice: written above, unless it has no key (or a bounded wait ran out)
+        if (p.n_splits == 1 && k0 < k1 && !*abort_flag) return;
         cluster_barrier();
         const uint32_t base = smem_u32(part);
         for (int idx = split * kDecThreads + threadIdx.x; idx < G * D; idx += p.n_splits * kDecThreads) {
@@ -635,7 +652,7 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = kCluster ? 2 : 1;
+    cfg.numAttrs = kCluster && a.n_splits > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, decode_split_kernel<D, kPaged, kSink, kCluster>, tk, tv, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
     if (kCluster) return ATTN_OK;
