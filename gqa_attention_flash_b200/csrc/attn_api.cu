@@ -838,6 +838,8 @@ attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts, cons
     if (R < 0) return ATTN_ERR_INVALID;
     attn_status_t st = validate_pool(num_blocks, block_size, max_blocks_per_seq);
     if (st != ATTN_OK) return st;
+    // the kernel counts and ranks empty entries in 32 bits
+    if ((long long)R * max_blocks_per_seq > 0x7fffffffll) return ATTN_ERR_INVALID;
     if (R == 0) return ATTN_OK;
     if (!block_tables || !ref_counts || !from_lens || !to_lens) return ATTN_ERR_NULL;
     if (!aligned4(block_tables) || !aligned16(ref_counts) || !aligned4(from_lens) ||

@@ -473,6 +473,7 @@ attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_
  * ATTN_ERR_DEVICE_BOUNDS; entries for which no page is left stay as they are and the call
  * flags ATTN_ERR_NO_PAGES.
  *   block_tables, ref_counts [in/out], from_lens, to_lens [in] int32 (R,).
+ * R * max_blocks_per_seq is below 2^31.
  */
 attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts,
                                 const int32_t *from_lens, const int32_t *to_lens, void *stream,

@@ -130,6 +130,15 @@ def test_cache_tables(binding):
     assert ext(rc=ctypes.c_void_p(24)) == INVALID
 
 
+def test_extend_refuses_tables_whose_entries_overflow_32_bits(binding):
+    # (lens = None: a size that is let through answers NULL, and nothing is launched)
+    ext = caller(binding.lib.attn_cache_extend, "bt rc lens to stream N nb bs mb", bt=P, rc=P,
+                 lens=None, to=P, stream=None, nb=10, bs=8)
+    assert ext(N=1 << 10, mb=1 << 21) == INVALID
+    assert ext(N=(1 << 31) - 1, mb=(1 << 28) - 1) == INVALID
+    assert ext(N=(1 << 10) - 1, mb=1 << 21) == NULL
+
+
 def test_binding_refuses_tensors_that_do_not_fit(binding):
     bf, i = torch.bfloat16, torch.int32
     z = torch.zeros
