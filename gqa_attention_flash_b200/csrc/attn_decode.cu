@@ -293,9 +293,11 @@ __global__ void __launch_bounds__(kDecThreads)
                             if (k >= n_chunks) break;
                             const int j = row + k * br;
                             if (edge && !vis.any(j, br)) continue;
-                            const int blk = cur[k];
-                            if (blk < 0 || blk >= p.num_blocks) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-                            // an out-of-range block reads as zeros (outside the tensor map)
+                            int blk = cur[k];
+                            if (blk < 0 || blk >= p.num_blocks) {
+                                record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+                                blk = -1;  // reads as zeros (before the tensor map's first row)
+                            }
                             const int prow = blk * (1 << p.block_shift) + (j & ((1 << p.block_shift) - 1));
                             // checked build: the chunk stays inside its tile of the ring (an
                             // out-of-range block is the documented zero-filled case)

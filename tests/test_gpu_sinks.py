@@ -380,3 +380,33 @@ def test_window_workload_rows():
         assert float((L[b:b + 1, :, rows].double() - lse).abs().max()) <= 2e-5
         assert torch.all(O[b, :, n:] == 0)
     assert math.isfinite(float(O.float().abs().max()))
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("block", [8, 16, 256])
+def test_pages_outside_the_pool_read_as_zeros(block, sinks):
+    """Whatever the page number, also one whose row number does not fit 32 bits."""
+    lens = [600, 300]
+    c = (2, 8, 2, 128, 0, lens, 1000, 4, 2, block)
+    Q, _, _, n, _, tables, Kp, Vp = decode_case(c, 0.0)
+
+    def run(t, K, V):
+        O = torch.full_like(Q, float("nan"))
+        if sinks:
+            binding.attn_decode_paged_sinks(O, Q, K, V, t, n, 1000, 4, 2)
+        else:
+            binding.attn_decode_paged(O, Q, K, V, t, n, 2)
+        return O
+
+    page = int(tables[0, 1])
+    Kz, Vz = Kp.clone(), Vp.clone()
+    Kz[page] = 0
+    Vz[page] = 0
+    want = run(tables, Kz, Vz)
+    assert binding.last_device_status() == 0
+    for bad in (-1, -(2 ** 31), Kp.shape[0], 2 ** 32 // block, 2 ** 31 - 1):
+        t = tables.clone()
+        t[0, 1] = bad
+        got = run(t, Kp, Vp)
+        assert binding.STATUS[binding.last_device_status()] == "ATTN_ERR_DEVICE_BOUNDS"
+        assert torch.equal(got, want), bad
