@@ -388,6 +388,10 @@ attn_status_t attn_fwd_sinks(void *O, const void *Q, const void *K, const void *
 
 namespace {
 
+// Most positions of a cache that the windowed decode and the tree accept: their kernels
+// add tile and slice offsets to positions in 32 bits.
+constexpr long long kMaxPositions = 1ll << 30;
+
 // attn_decode (window = 0) and attn_decode_sinks.
 attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const void *V,
                                 const int32_t *lengths, int window, int sinks, int n_splits,
@@ -454,7 +458,7 @@ attn_status_t attn_decode_sinks(void *O, const void *Q, const void *K, const voi
                                 const int32_t *lengths, int window, int sinks, int n_splits,
                                 void *stream, int B, int Hq, int Hkv, int S_cap, int D) {
     NvtxRange nvtx_range("attn_decode_sinks");
-    if (window < 1 || sinks < 0) return ATTN_ERR_INVALID;
+    if (window < 1 || sinks < 0 || S_cap > kMaxPositions) return ATTN_ERR_INVALID;
     if (n_splits == 0 && B >= 0 && Hkv >= 1 && S_cap >= 0)
         n_splits = sink_splits(B, Hkv, S_cap, window, sinks);
     return decode_contiguous(O, Q, K, V, lengths, window, sinks, n_splits, stream, B, Hq, Hkv, S_cap,
@@ -671,6 +675,7 @@ attn_status_t attn_decode_paged_sinks(void *O, const void *Q, const void *K_cach
                                       int block_size, int max_blocks_per_seq, int D) {
     NvtxRange nvtx_range("attn_decode_paged_sinks");
     if (window < 1 || sinks < 0) return ATTN_ERR_INVALID;
+    if ((long long)max_blocks_per_seq * block_size > kMaxPositions) return ATTN_ERR_INVALID;
     if (n_splits == 0 && B >= 0 && Hkv >= 1 && max_blocks_per_seq >= 0 && block_size > 0)
         n_splits = sink_splits(B, Hkv, (long long)max_blocks_per_seq * block_size, window, sinks);
     return decode_paged(O, Q, K_cache, V_cache, block_tables, seq_lens, window, sinks, n_splits, stream,
@@ -686,6 +691,7 @@ attn_status_t attn_tree_paged(void *O, const void *Q, const void *K_cache, const
     if (B < 0 || Hq < 1 || Hkv < 1 || T < 0 || T > 256) return ATTN_ERR_INVALID;
     attn_status_t st = validate_pool(num_blocks, block_size, max_blocks_per_seq);
     if (st != ATTN_OK) return st;
+    if ((long long)max_blocks_per_seq * block_size > kMaxPositions) return ATTN_ERR_INVALID;
     if (Hq % Hkv != 0 || Hq / Hkv > 16) return ATTN_ERR_INVALID;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
     if ((long long)B * Hkv > 0x7fffffffll) return ATTN_ERR_INVALID;

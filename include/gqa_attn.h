@@ -342,8 +342,8 @@ attn_status_t attn_decode_noalloc(void *O, const void *Q, const void *K, const v
  * of block_tables for pages without a visible key may hold anything (attn_cache_free
  * leaves -1 there), and those pages are not read.
  * Arguments and errors as attn_decode / attn_decode_paged; window >= 1, sinks >= 0;
- * n_splits 0..64, 0 = chosen by the library from the sizes.  Up to 8 slices need no
- * workspace.
+ * n_splits 0..64, 0 = chosen by the library from the sizes; S_cap, or
+ * max_blocks_per_seq * block_size, at most 2^30.  Up to 8 slices need no workspace.
  */
 attn_status_t attn_decode_sinks(void *O, const void *Q, const void *K, const void *V,
                                 const int32_t *lengths, int window, int sinks, int n_splits,
@@ -376,7 +376,8 @@ attn_status_t attn_decode_paged_sinks(void *O, const void *Q, const void *K_cach
  * each is flagged ATTN_ERR_DEVICE_BOUNDS.  Cache rows at or past context_lens[b] +
  * draft_lens[b] never reach O; those before it must hold finite values.
  *   Sizes: B >= 0; T 0..256; Hq, Hkv >= 1, Hq % Hkv == 0, Hq / Hkv <= 16;
- *          max_blocks_per_seq >= 1; block_size a power of two >= 8; D in {64, 128}.
+ *          max_blocks_per_seq >= 1; block_size a power of two >= 8; D in {64, 128};
+ *          max_blocks_per_seq * block_size at most 2^30.
  * Allocates a stream-ordered workspace (partial results of the sequences that several
  * SMs share, up to 39 MB, and B + 1 integers).
  */

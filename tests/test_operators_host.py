@@ -130,6 +130,23 @@ def test_cache_tables(binding):
     assert ext(rc=ctypes.c_void_p(24)) == INVALID
 
 
+def test_caches_past_2_30_positions_are_refused(binding):
+    # (O = None: a size that is let through answers NULL, and nothing is launched)
+    L = binding.lib
+    con = caller(L.attn_decode_sinks, "O Q K V lens window sinks n stream B Hq Hkv cap D", O=None, Q=P,
+                 K=P, V=P, lens=P, window=8, sinks=2, n=0, stream=None, B=1, Hq=8, Hkv=2, D=128)
+    pag = caller(L.attn_decode_paged_sinks, "O Q K V bt lens window sinks n stream B Hq Hkv nb bs mb D",
+                 O=None, Q=P, K=P, V=P, bt=P, lens=P, window=8, sinks=2, n=0, stream=None, B=1, Hq=8,
+                 Hkv=2, nb=10, bs=16, D=128)
+    tree = caller(L.attn_tree_paged, "O Q K V bt ctx par dl stream B Hq Hkv T nb bs mb D", O=None,
+                  Q=P, K=P, V=P, bt=P, ctx=P, par=P, dl=None, stream=None, B=1, Hq=8, Hkv=2, T=4,
+                  nb=10, bs=16, D=128)
+    assert con(cap=2 ** 30) == NULL and con(cap=2 ** 30 + 1) == INVALID
+    for f in (pag, tree):
+        assert f(mb=2 ** 26) == NULL
+        assert f(mb=2 ** 26 + 1) == INVALID and f(mb=2 ** 27 - 1) == INVALID
+
+
 def test_extend_refuses_tables_whose_entries_overflow_32_bits(binding):
     # (lens = None: a size that is let through answers NULL, and nothing is launched)
     ext = caller(binding.lib.attn_cache_extend, "bt rc lens to stream N nb bs mb", bt=P, rc=P,
