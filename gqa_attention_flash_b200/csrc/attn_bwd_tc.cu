@@ -1113,11 +1113,13 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     if (cudaEventRecord(ss->fork, stream) != cudaSuccess ||
         cudaStreamWaitEvent(ss->s, ss->fork, 0) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    if (!launch_dq(ss->s) || !launch_dkdv()) return ATTN_ERR_CUDA;
-    if (cudaEventRecord(ss->join, ss->s) != cudaSuccess ||
-        cudaStreamWaitEvent(stream, ss->join, 0) != cudaSuccess)
-        return ATTN_ERR_CUDA;
-    return ATTN_OK;
+    const bool launched = launch_dq(ss->s) && launch_dkdv();
+    // Joined also where a launch failed: dQ may be running, and the caller gives back the
+    // workspace that it reads.  Without a join the host waits for it.
+    const bool joined = cudaEventRecord(ss->join, ss->s) == cudaSuccess &&
+                        cudaStreamWaitEvent(stream, ss->join, 0) == cudaSuccess;
+    if (!joined) cudaStreamSynchronize(ss->s);
+    return launched && joined ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
