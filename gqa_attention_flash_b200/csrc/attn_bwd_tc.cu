@@ -993,6 +993,26 @@ SideStream *side_stream() {
     return per_dev[dev];
 }
 
+// Stream-ordered workspace, given back on every way out.
+struct Workspace {
+    void *ptr = nullptr;
+    cudaStream_t stream;
+    explicit Workspace(cudaStream_t s) : stream(s) {}
+    ~Workspace() { release(); }
+    Workspace(const Workspace &) = delete;
+    Workspace &operator=(const Workspace &) = delete;
+    bool alloc(size_t bytes) {
+        if (workspace_alloc(&ptr, bytes, stream) == cudaSuccess) return true;
+        ptr = nullptr;
+        return false;
+    }
+    bool release() {
+        void *p = ptr;
+        ptr = nullptr;
+        return !p || cudaFreeAsync(p, stream) == cudaSuccess;
+    }
+};
+
 template <int D, bool kSink>
 attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     using C = TcCfg<D>;
@@ -1034,7 +1054,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     if (grid > 0x7fffffffll) return ATTN_ERR_INVALID;
     const int n_kt = (a.Sk + TB - 1) / TB, pairs = a.Hkv * a.B;
     long long grid_kv = (long long)n_kt * pairs, reduce = 0;
-    void *part = nullptr;
+    Workspace part(stream);
     p.part = nullptr;
     p.sink_tiles = 0;
     p.split_sink = p.split_win = 1;
@@ -1066,9 +1086,8 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
         if (p.split_win > 1) reduce += others;
         if (reduce > 0) {
             const long long slots = p.split_win > 1 ? grid_kv : sink_ctas;
-            if (workspace_alloc(&part, (size_t)slots * 2 * TB * D * sizeof(float), stream) != cudaSuccess)
-                return ATTN_ERR_CUDA;
-            p.part = static_cast<float *>(part);
+            if (!part.alloc((size_t)slots * 2 * TB * D * sizeof(float))) return ATTN_ERR_CUDA;
+            p.part = static_cast<float *>(part.ptr);
         }
     }
     if (grid_kv > 0x7fffffffll) return ATTN_ERR_INVALID;
@@ -1100,7 +1119,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
             if (ok && reduce > 0)
                 ok = launch(bwd_dkdv_reduce_kernel<D>, dim3(static_cast<unsigned>(reduce), TB / 16), 256, 0,
                             stream, p);
-            if (part && cudaFreeAsync(part, stream) != cudaSuccess) ok = false;
+            ok = part.release() && ok;
         }
         return ok;
     };

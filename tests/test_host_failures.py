@@ -85,6 +85,8 @@ def backward(B, Hq, Hkv, S, D, window, sinks):
 
 CALLS = {
     "backward, two streams": backward(4, 32, 8, 4096, 128, 1024, 4),
+    "backward, two streams, split": backward(1, 32, 1, 1300, 64, 64, 4),
+    "backward, one stream, split": backward(2, 8, 2, 1000, 64, 200, 5),
     "backward, plain": lambda L: L.attn_bwd(P, P, P, P, P, P, P, P, P, 1, 8, 2, 2048, 2048, 128, f(0.1), 1, 0,
                                             0, None, None, STREAM),
     "forward": lambda L: L.attn_fwd_sinks(P, P, P, P, P, 1, 8, 2, 300, 300, 128, f(0.1), 64, 4, 0, None, None,
