@@ -1119,11 +1119,11 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
             if (ok && reduce > 0)
                 ok = launch(bwd_dkdv_reduce_kernel<D>, dim3(static_cast<unsigned>(reduce), TB / 16), 256, 0,
                             stream, p);
-            ok = part.release() && ok;
         }
         return ok;
     };
-    if (one_stream) return launch_dq(stream) && launch_dkdv() ? ATTN_OK : ATTN_ERR_CUDA;
+    if (one_stream)
+        return launch_dq(stream) && launch_dkdv() && part.release() ? ATTN_OK : ATTN_ERR_CUDA;
     // dK/dV and dQ are independent: run dQ on a side stream so that each kernel's
     // last wave overlaps the other's work.
     SideStream *ss = side_stream();
@@ -1138,7 +1138,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     const bool joined = cudaEventRecord(ss->join, ss->s) == cudaSuccess &&
                         cudaStreamWaitEvent(stream, ss->join, 0) == cudaSuccess;
     if (!joined) cudaStreamSynchronize(ss->s);
-    return launched && joined ? ATTN_OK : ATTN_ERR_CUDA;
+    return launched && joined && part.release() ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
