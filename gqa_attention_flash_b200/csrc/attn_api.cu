@@ -205,8 +205,8 @@ __global__ void wait_probe_kernel(uint64_t limit_ns) {
 }  // namespace
 
 attn_status_t launch_wait_probe(int limit_us, cudaStream_t stream) {
-    wait_probe_kernel<<<1, 32, 0, stream>>>(static_cast<uint64_t>(limit_us) * 1000ull);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return launch_kernel(wait_probe_kernel, dim3(1), 32, 0, stream,
+                         static_cast<uint64_t>(limit_us) * 1000ull);
 }
 
 }  // namespace gqa
@@ -287,7 +287,7 @@ attn_status_t attn_fwd_varlen(void *O, const void *Q, const void *K, const void 
         a.V = Q;
         a.Sk = 0;
     }
-    return launch_fwd(a, static_cast<cudaStream_t>(stream));
+    return answer(launch_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_fwd(void *O, const void *Q, const void *K, const void *V, float *LSE, int B,
@@ -350,8 +350,9 @@ attn_status_t attn_fwd_flex(void *O, const void *Q, const void *K, const void *V
         a.doc_q = nullptr;
         a.block_mask = nullptr;
     }
-    if (gqa::bsparse_eligible(a)) return gqa::launch_fwd_bsparse(a, static_cast<cudaStream_t>(stream));
-    return launch_fwd(a, static_cast<cudaStream_t>(stream));
+    if (gqa::bsparse_eligible(a))
+        return answer(gqa::launch_fwd_bsparse(a, static_cast<cudaStream_t>(stream)));
+    return answer(launch_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_fwd_sinks(void *O, const void *Q, const void *K, const void *V, float *LSE,
@@ -383,7 +384,7 @@ attn_status_t attn_fwd_sinks(void *O, const void *Q, const void *K, const void *
     a.window = window;
     a.sinks = sinks;
     a.input_pos = input_pos;
-    return launch_fwd(a, static_cast<cudaStream_t>(stream));
+    return answer(launch_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -411,7 +412,7 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
     const size_t bytes = decode_workspace_floats(B, Hq, n_splits, D) * sizeof(float);
     const bool needs_ws = window == 0 || !decode_sinks_in_cluster(n_splits);
     void *ws = nullptr;
-    if (needs_ws && workspace_alloc(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (needs_ws && workspace_alloc(&ws, bytes, s) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     DecodeArgs a;
     a.O = O;
     a.Q = Q;
@@ -429,7 +430,7 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
     a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
     if (needs_ws && cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
-    return st;
+    return answer(st);
 }
 
 // Slices per (sequence, KV head) when the caller leaves them to the library: enough for
@@ -489,12 +490,12 @@ attn_status_t backward(void *dQ, void *dK, void *dV, const void *dO, const void 
             const size_t bytes = (size_t)rows_k * D * 2;
             if (cudaMemsetAsync(dK, 0, bytes, s) != cudaSuccess ||
                 cudaMemsetAsync(dV, 0, bytes, s) != cudaSuccess)
-                return ATTN_ERR_CUDA;
+                return answer(ATTN_ERR_CUDA);
         }
         return ATTN_OK;
     }
     void *ws = nullptr;
-    if (workspace_alloc(&ws, (size_t)rows_q * sizeof(float), s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (workspace_alloc(&ws, (size_t)rows_q * sizeof(float), s) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     BwdArgs a;
     a.dQ = dQ;
     a.dK = dK;
@@ -521,7 +522,7 @@ attn_status_t backward(void *dQ, void *dK, void *dV, const void *dO, const void 
     a.delta = static_cast<float *>(ws);
     st = launch_bwd(a, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
-    return st;
+    return answer(st);
 }
 
 }  // namespace
@@ -567,7 +568,7 @@ attn_status_t attn_rbs_block_mask(uint8_t *block_mask, float *base_scores, float
     const size_t ws_floats = (size_t)B * Hkv * nkb * (D + 2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *ws = nullptr;
-    if (workspace_alloc(&ws, ws_floats * sizeof(float), s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (workspace_alloc(&ws, ws_floats * sizeof(float), s) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     RbsArgs a;
     a.Q = Q;
     a.K = K;
@@ -588,7 +589,7 @@ attn_status_t attn_rbs_block_mask(uint8_t *block_mask, float *base_scores, float
     a.beta = a.rad + (size_t)B * Hkv * nkb;
     attn_status_t st = launch_rbs(a, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
-    return st;
+    return answer(st);
 }
 
 namespace {
@@ -618,7 +619,7 @@ attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const vo
     const size_t bytes = decode_workspace_floats(B, Hq, n_splits, D) * sizeof(float);
     const bool needs_ws = window == 0 || !decode_sinks_in_cluster(n_splits);
     void *ws = nullptr;
-    if (needs_ws && workspace_alloc(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (needs_ws && workspace_alloc(&ws, bytes, s) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     DecodeArgs a;
     a.O = O;
     a.Q = Q;
@@ -640,7 +641,7 @@ attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const vo
     a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
     if (needs_ws && cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
-    return st;
+    return answer(st);
 }
 
 // Sizes of a paged cache that every operator on it checks.
@@ -719,7 +720,7 @@ attn_status_t attn_tree_paged(void *O, const void *Q, const void *K_cache, const
     a.num_blocks = num_blocks;
     a.block_size = block_size;
     a.max_blocks = max_blocks_per_seq;
-    return launch_tree(a, static_cast<cudaStream_t>(stream));
+    return answer(launch_tree(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_cache_append(void *K_cache, void *V_cache, const void *K_new, const void *V_new,
@@ -751,7 +752,7 @@ attn_status_t attn_cache_append(void *K_cache, void *V_cache, const void *K_new,
     a.num_blocks = num_blocks;
     a.block_size = block_size;
     a.max_blocks = max_blocks_per_seq;
-    return launch_cache_append(a, static_cast<cudaStream_t>(stream));
+    return answer(launch_cache_append(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_cache_compact(void *K_cache, void *V_cache, const int32_t *block_tables,
@@ -782,7 +783,7 @@ attn_status_t attn_cache_compact(void *K_cache, void *V_cache, const int32_t *bl
     a.num_blocks = num_blocks;
     a.block_size = block_size;
     a.max_blocks = max_blocks_per_seq;
-    return launch_cache_compact(a, static_cast<cudaStream_t>(stream));
+    return answer(launch_cache_compact(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_cache_copy_blocks(void *K_cache, void *V_cache, const int32_t *src,
@@ -797,8 +798,9 @@ attn_status_t attn_cache_copy_blocks(void *K_cache, void *V_cache, const int32_t
     if (!K_cache || !V_cache || !src || !dst) return ATTN_ERR_NULL;
     if (!aligned16(K_cache) || !aligned16(V_cache) || !aligned4(src) || !aligned4(dst))
         return ATTN_ERR_INVALID;
-    return launch_cache_copy(K_cache, V_cache, src, dst, N, num_blocks,
-                             (long long)block_size * Hkv * D * 2, static_cast<cudaStream_t>(stream));
+    return answer(launch_cache_copy(K_cache, V_cache, src, dst, N, num_blocks,
+                                    (long long)block_size * Hkv * D * 2,
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_t *seq_lens,
@@ -817,7 +819,7 @@ attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_
         return ATTN_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *ws = nullptr;
-    if (workspace_alloc(&ws, (size_t)N * sizeof(int32_t), s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (workspace_alloc(&ws, (size_t)N * sizeof(int32_t), s) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     CacheForkArgs a;
     a.tables = block_tables;
     a.refs = ref_counts;
@@ -834,7 +836,7 @@ attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_
     a.workspace = static_cast<int32_t *>(ws);
     st = launch_cache_fork(a, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
-    return st;
+    return answer(st);
 }
 
 attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts, const int32_t *from_lens,
@@ -854,7 +856,7 @@ attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long ints = R + 1ll + std::min((long long)R * max_blocks_per_seq, (long long)num_blocks);
     void *ws = nullptr;
-    if (workspace_alloc(&ws, (size_t)ints * sizeof(int32_t), s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (workspace_alloc(&ws, (size_t)ints * sizeof(int32_t), s) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     CacheExtendArgs a;
     a.tables = block_tables;
     a.refs = ref_counts;
@@ -867,7 +869,7 @@ attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts, cons
     a.workspace = static_cast<int32_t *>(ws);
     st = launch_cache_extend(a, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
-    return st;
+    return answer(st);
 }
 
 attn_status_t attn_cache_free(int32_t *block_tables, int32_t *ref_counts, const int32_t *rows,
@@ -880,8 +882,8 @@ attn_status_t attn_cache_free(int32_t *block_tables, int32_t *ref_counts, const 
     if (!aligned4(block_tables) || !aligned4(ref_counts) || !aligned4(rows) || !aligned4(first) ||
         !aligned4(last))
         return ATTN_ERR_INVALID;
-    return launch_cache_free(block_tables, ref_counts, rows, first, last, N, R, max_blocks_per_seq,
-                             num_blocks, static_cast<cudaStream_t>(stream));
+    return answer(launch_cache_free(block_tables, ref_counts, rows, first, last, N, R, max_blocks_per_seq,
+                                    num_blocks, static_cast<cudaStream_t>(stream)));
 }
 
 const char *attn_status_string(attn_status_t status) {
@@ -903,17 +905,17 @@ const char *attn_status_string(attn_status_t status) {
 
 attn_status_t attn_last_device_status(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return ATTN_ERR_CUDA;
+        return answer(ATTN_ERR_CUDA);
     int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     const int zero = 0;
-    if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return answer(ATTN_ERR_CUDA);
     return static_cast<attn_status_t>(v);
 }
 
 attn_status_t attn_check_bounded_wait(int limit_us, void *stream) {
     if (limit_us < 1 || limit_us > 2000000) return ATTN_ERR_INVALID;
-    return launch_wait_probe(limit_us, static_cast<cudaStream_t>(stream));
+    return answer(launch_wait_probe(limit_us, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -55,10 +55,10 @@ attn_status_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     if (rows > 0) {
         const long long blocks = (rows + 256 / (D / 8) - 1) / (256 / (D / 8));
         if (blocks > 0x7fffffffll) return ATTN_ERR_INVALID;
-        bwd_delta_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-            static_cast<const __nv_bfloat16 *>(a.dO), static_cast<const __nv_bfloat16 *>(a.O), a.delta,
-            rows);
-        if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+        const attn_status_t st = launch_kernel(
+            bwd_delta_kernel<D>, dim3(static_cast<unsigned>(blocks)), 256, 0, stream,
+            static_cast<const __nv_bfloat16 *>(a.dO), static_cast<const __nv_bfloat16 *>(a.O), a.delta, rows);
+        if (st != ATTN_OK) return st;
     }
     return launch_bwd_tc(a, stream);
 }

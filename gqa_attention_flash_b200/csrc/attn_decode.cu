@@ -665,7 +665,7 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     if (cudaLaunchKernelEx(&cfg, decode_combine_kernel<D>, static_cast<__nv_bfloat16 *>(a.O),
                            static_cast<const float *>(a.workspace), BH, a.n_splits) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return ATTN_OK;
 }
 
 }  // namespace

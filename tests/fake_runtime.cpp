@@ -41,6 +41,8 @@ void fake_reset(int fail_at) {
     g_last = cudaSuccess;
     g_fail_at = fail_at;
 }
+void fake_set_last_error(int e) { g_last = static_cast<cudaError_t>(e); }
+int fake_last_error() { return static_cast<int>(g_last); }
 int fake_calls() { return g_calls; }
 int fake_log_size() { return static_cast<int>(g_log.size()); }
 void fake_log(int i, int *kind, const void **stream, const void **what) {

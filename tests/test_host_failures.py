@@ -123,3 +123,16 @@ def test_a_failing_cuda_call(objects, name):
                 break
             assert rc == CUDA, f"{name}: call {at} of {first} fails, and the answer is {rc}"
             check_log(lib, f"{name}: call {at} of {first} fails")
+            # the runtime's last error is clean again, for this library's calls and any other's
+            assert lib.fake_last_error() == 0, f"{name}: call {at} of {first} fails"
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_an_error_of_other_code_is_not_the_calls(objects, name):
+    """An error that the process left with the runtime before the call is neither reported nor
+    cleared by it."""
+    lib = fresh(objects)
+    lib.fake_reset(-1)
+    lib.fake_set_last_error(2)
+    assert CALLS[name](lib) == OK
+    assert lib.fake_last_error() == 2
