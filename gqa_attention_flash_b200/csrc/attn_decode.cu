@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kDecThreads)
                     sum += wt;
                     o = fmaf(wt, v[s], o);
                 }
-            p.O[(long long)(b * p.Hq + h0) * D + idx] = __float2bfloat16_rn(sum > 0.f ? o / sum : 0.f);
+            // no key in any slice: 0; a sum that is NaN is no empty one and reaches the output
+            p.O[(long long)(b * p.Hq + h0) * D + idx] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
         }
         cluster_barrier();  // no CTA leaves while another reads its partials
     }
@@ -561,7 +562,12 @@ __global__ void __launch_bounds__(128)
     if (idx >= BH) return;
     const float *part = ws + (long long)idx * n_splits * WS;
     float M = neg_inf();
-    for (int s = lane; s < n_splits; s += 32) M = fmaxf(M, part[s * WS + D]);
+    bool some = false;  // a slice with a key (its log-sum-exp may be NaN, which M passes over)
+    for (int s = lane; s < n_splits; s += 32) {
+        const float lse = part[s * WS + D];
+        M = fmaxf(M, lse);
+        some = some || lse != neg_inf();
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     constexpr int PER = D / 32;  // output elements per lane
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = 0.f;
     __nv_bfloat16 *out = O + (long long)idx * D + lane * PER;
-    if (M == neg_inf()) {  // no valid key in any slice
+    if (!__any_sync(0xffffffffu, some)) {  // no valid key in any slice
 #pragma unroll
         for (int k = 0; k < PER; ++k) out[k] = __float2bfloat16_rn(0.f);
         return;
