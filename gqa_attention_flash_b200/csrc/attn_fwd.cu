@@ -932,7 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (have && !warp_wait(bar_o, (n_it + n_done - 1) & 1, abort_flag, p.wait_limit_ns,
                                    p.status))
                 have = false;
-            const bool out_valid = have && row < q_end && l > 0.f;
+            // l = 0: no visible key (a sum that is NaN is none such, and reaches O and LSE)
+            const bool out_valid = have && row < q_end && l != 0.f;
             const float inv_l = out_valid ? 1.f / l : 0.f;
             __nv_bfloat16 *orow = p.O + ((long long)(it.b * p.Hq + it.hq) * p.Sq + row) * D;
             if (have) {

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         bool have = ok && n > 0;
         if (have && !warp_wait(bar(C::BAR_ODONE), (n - 1) & 1, abort_flag, p.wait_limit_ns, p.status))
             have = false;
-        const bool out_valid = have && l > 0.f;
+        const bool out_valid = have && l != 0.f;  // NaN is no empty row
         const float inv_l = out_valid ? 1.f / l : 0.f;
         __nv_bfloat16 *orow = p.O + ((long long)(b * p.Hq + hq) * p.Sq + row) * D;
         if (have) {

@@ -618,9 +618,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     l = a0 * l + a1 * ml[TM + r];
                 }
             }
-            // a whole segment's factors carry 1 / sum; -1 marks a row that is zero
+            // a whole segment's factors carry 1 / sum; -1 marks a row that is zero (a sum that
+            // is NaN reaches the row)
             if (whole && (kTwo || t == 0)) {
-                const bool some = l > 0.f && draft < w.len.drafts;
+                const bool some = l != 0.f && draft < w.len.drafts;
                 a0 = some ? a0 / l : -1.f;
                 a1 = some ? a1 / l : -1.f;
             }
@@ -744,7 +745,10 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const float grown = fmaxf(M, top);
-                if (grown == ninf()) continue;
+                if (grown == ninf()) {  // no key seen so far, or NaN scores alone
+                    lsum += l;
+                    continue;
+                }
                 const float old = fast_exp2(M - grown);  // 0 for the first batch
                 M = grown;
                 const float wt = fast_exp2(m - M);
@@ -766,12 +770,12 @@ __global__ void __launch_bounds__(kCombineThreads)
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
-            if (lsum > 0.f && row % p.T < len.drafts) inv = 1.f / lsum;
+            if (lsum != 0.f && row % p.T < len.drafts) inv = 1.f / lsum;
         }
 #pragma unroll
         for (int x = 0; x < PER; x += 2)
             *reinterpret_cast<uint32_t *>(out + x) =
-                inv > 0.f ? pack_bf16x2(acc[x] * inv, acc[x + 1] * inv) : 0u;
+                inv != 0.f ? pack_bf16x2(acc[x] * inv, acc[x + 1] * inv) : 0u;
     }
 }
 
