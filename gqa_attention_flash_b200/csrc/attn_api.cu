@@ -399,7 +399,7 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
                                 void *stream, int B, int Hq, int Hkv, int S_cap, int D) {
     if (B < 0 || Hq < 1 || Hkv < 1 || S_cap < 0 || n_splits < 1 || n_splits > 64)
         return ATTN_ERR_INVALID;
-    if (Hq % Hkv != 0 || Hq / Hkv > 16) return ATTN_ERR_INVALID;
+    if (Hq % Hkv != 0 || Hq / Hkv > 16 || Hkv > 65535) return ATTN_ERR_INVALID;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
     if (B == 0) return ATTN_OK;
     if (!O || !Q || !lengths) return ATTN_ERR_NULL;
@@ -604,7 +604,7 @@ attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const vo
         return ATTN_ERR_INVALID;
     if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1)) != 0)
         return ATTN_ERR_INVALID;
-    if (Hq % Hkv != 0 || Hq / Hkv > 16) return ATTN_ERR_INVALID;
+    if (Hq % Hkv != 0 || Hq / Hkv > 16 || Hkv > 65535) return ATTN_ERR_INVALID;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
     if ((long long)num_blocks * block_size > 0x7fffffffll ||
         (long long)max_blocks_per_seq * block_size > 0x7fffffffll)

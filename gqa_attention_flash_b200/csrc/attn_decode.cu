@@ -71,6 +71,7 @@ struct DecCfg {
     static constexpr int WS_STRIDE = D + 4;     // floats per partial: o[D], lse, pad
 };
 
+constexpr int kMaxGridZ = 65535;
 constexpr int kMaxCluster = 8;  // slices of one cluster (the portable cluster size)
 
 struct DecParams {
@@ -79,6 +80,7 @@ struct DecParams {
     float *ws;
     const int32_t *lengths;
     int B, Hq, Hkv, S_cap, group, n_splits;
+    int b0;  // sequence of blockIdx.z = 0
     float scale_log2;
     uint64_t wait_limit_ns;
     int *status;  // device status word
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kDecThreads)
 
     const int split = blockIdx.x;
     const int hkv = blockIdx.y;
-    const int b = blockIdx.z;
+    const int b = p.b0 + blockIdx.z;
     const int G = p.group;
     const int h0 = hkv * G;
     const int warp = threadIdx.x >> 5;
@@ -655,14 +657,18 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.n_splits, a.Hkv, a.B);
     cfg.blockDim = dim3(kDecThreads, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = kCluster && a.n_splits > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, decode_split_kernel<D, kPaged, kSink, kCluster>, tk, tv, p) != cudaSuccess)
-        return ATTN_ERR_CUDA;
+    // a grid's z dimension ends at 65535: more sequences take several launches
+    for (p.b0 = 0; p.b0 < a.B; p.b0 += kMaxGridZ) {
+        cfg.gridDim = dim3(a.n_splits, a.Hkv, min(a.B - p.b0, kMaxGridZ));
+        if (cudaLaunchKernelEx(&cfg, decode_split_kernel<D, kPaged, kSink, kCluster>, tk, tv, p) !=
+            cudaSuccess)
+            return ATTN_ERR_CUDA;
+    }
     if (kCluster) return ATTN_OK;
     const int BH = a.B * a.Hq;
     cfg.gridDim = dim3((BH + 3) / 4, 1, 1);

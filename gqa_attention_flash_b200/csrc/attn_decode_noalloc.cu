@@ -76,7 +76,7 @@ extern "C" attn_status_t attn_decode_noalloc(void *O, const void *Q, const void 
     // Same argument checks as attn_decode.
     if (B < 0 || Hq < 1 || Hkv < 1 || S_cap < 0 || n_splits < 1 || n_splits > 64)
         return ATTN_ERR_INVALID;
-    if (Hq % Hkv != 0 || Hq / Hkv > 16) return ATTN_ERR_INVALID;
+    if (Hq % Hkv != 0 || Hq / Hkv > 16 || Hkv > 65535) return ATTN_ERR_INVALID;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
     if (B == 0) return ATTN_OK;
     if (!O || !Q || !lengths) return ATTN_ERR_NULL;

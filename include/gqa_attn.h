@@ -267,7 +267,7 @@ attn_status_t attn_block_mask_document(uint8_t *out, int Sq, int Sk, int input_p
  *                  clamped and flagged ATTN_ERR_DEVICE_BOUNDS; values <= 0
  *                  give O = 0 for that sequence.
  *   n_splits 1..64.
- *   Sizes: B >= 0; Hq, Hkv >= 1, Hq % Hkv == 0, Hq / Hkv <= 16;
+ *   Sizes: B >= 0; Hq, Hkv >= 1, Hq % Hkv == 0, Hq / Hkv <= 16, Hkv <= 65535;
  *          S_cap >= 0; D in {64, 128}.
  *
  * The per-slice partial results live in a workspace of
