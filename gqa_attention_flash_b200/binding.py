@@ -96,6 +96,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _i32(v, name):
+    """An integer of the C ABI (ctypes would cut a wider one to its low 32 bits: 2**32 sinks
+    to none)."""
+    v = int(v)
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{name} = {v} does not fit in 32 bits")
+    return v
+
+
 # The C ABI sees raw pointers and sizes only: it cannot tell a transposed view, a
 # float16 tensor or a tensor on another device from the layout it expects.  The
 # wrappers therefore refuse such tensors here, before any call into the library.
@@ -199,10 +208,12 @@ def attn_fwd(O, Q, K, V, LSE, scale, causal=False, window=0, input_pos=0, k_leng
     Shapes are read from the tensors: Q (B,Hq,Sq,D), K/V (B,Hkv,Sk,D).  Calls
     ``attn_fwd_varlen`` when q_lengths is given, else ``attn_fwd``.
     """
+    window = _i32(window, "window")
+    input_pos = _i32(input_pos, "input_pos")
     B, Hq, Hkv, Sq, Sk, D = _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths)
     _same_device(O=O, Q=Q, K=K, V=V, LSE=LSE, k_lengths=k_lengths, q_lengths=q_lengths)
     args = [_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale),
-            int(causal), int(window), int(input_pos), _ptr(k_lengths)]
+            int(causal), window, input_pos, _ptr(k_lengths)]
     if q_lengths is not None:
         rc = lib.attn_fwd_varlen(*args, _ptr(q_lengths), _stream(stream))
         _check(rc, "attn_fwd_varlen")
@@ -218,6 +229,8 @@ def attn_fwd_flex(O, Q, K, V, LSE, scale, causal=False, window=0, input_pos=0, k
     AliBiScore (alibi_slopes, fp32 (Hq,)), DocumentMask (doc_q int32 (Sq,), doc_kv
     int32 (Sk,)) and a BlockMask (uint8 (ceil(Sq/64), ceil(Sk/64)), or one per
     (batch, query head) as a 4-D (B, Hq, ., .) tensor), all on the device."""
+    window = _i32(window, "window")
+    input_pos = _i32(input_pos, "input_pos")
     B, Hq, Hkv, Sq, Sk, D = _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths)
     if alibi_slopes is not None:
         _tensor(alibi_slopes, "alibi_slopes", torch.float32, (Hq,))
@@ -232,7 +245,7 @@ def attn_fwd_flex(O, Q, K, V, LSE, scale, causal=False, window=0, input_pos=0, k
     _same_device(O=O, Q=Q, K=K, V=V, LSE=LSE, k_lengths=k_lengths, q_lengths=q_lengths,
                  alibi_slopes=alibi_slopes, doc_q=doc_q, doc_kv=doc_kv, block_mask=block_mask)
     rc = lib.attn_fwd_flex(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D,
-                           float(scale), int(causal), int(window), int(input_pos),
+                           float(scale), int(causal), window, input_pos,
                            _ptr(k_lengths), _ptr(q_lengths), float(softcap), _ptr(alibi_slopes),
                            _ptr(doc_q), _ptr(doc_kv), _ptr(block_mask),
                            1 if block_mask is not None and block_mask.dim() == 4 else 0,
@@ -244,6 +257,7 @@ def rbs_block_mask(Q, K, alpha_base=0.22, alpha_rescue=0.18, diagonal=1, want_sc
                    stream=None):
     """Block-sparse prefill mask from the RBS block scores: uint8 (B, Hq, nqb, nkb)
     device tensor (2 = keep, 0 = skip), plus the (base, rescue) scores if asked."""
+    diagonal = _i32(diagonal, "diagonal")
     B, Hq, Sq, D = _tensor(Q, "Q", torch.bfloat16, 4)
     _, Hkv, Sk, _ = _tensor(K, "K", torch.bfloat16, (B, None, None, D))
     _same_device(Q=Q, K=K)
@@ -253,7 +267,7 @@ def rbs_block_mask(Q, K, alpha_base=0.22, alpha_rescue=0.18, diagonal=1, want_sc
     resc = torch.empty(shape, dtype=torch.float32, device=Q.device) if want_scores else None
     rc = lib.attn_rbs_block_mask(_ptr(mask), _ptr(base), _ptr(resc), _ptr(Q), _ptr(K), B, Hq,
                                  Hkv, Sq, Sk, D, float(alpha_base), float(alpha_rescue),
-                                 int(diagonal), _stream(stream))
+                                 diagonal, _stream(stream))
     _check(rc, "attn_rbs_block_mask")
     return (mask, base, resc) if want_scores else mask
 
@@ -262,10 +276,12 @@ def attn_bwd(dQ, dK, dV, dO, Q, K, V, O, LSE, scale, causal=False, window=0, inp
              k_lengths=None, q_lengths=None, stream=None):
     """Backward of attn_fwd: fill dQ (like Q) and dK, dV (like K, V) in place from dO,
     the forward's inputs, output O and LSE."""
+    window = _i32(window, "window")
+    input_pos = _i32(input_pos, "input_pos")
     B, Hq, Hkv, Sq, Sk, D = _check_backward(dQ, dK, dV, dO, Q, K, V, O, LSE, k_lengths, q_lengths)
     rc = lib.attn_bwd(_ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
-                      _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale), int(causal), int(window),
-                      int(input_pos), _ptr(k_lengths), _ptr(q_lengths), _stream(stream))
+                      _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale), int(causal), window,
+                      input_pos, _ptr(k_lengths), _ptr(q_lengths), _stream(stream))
     _check(rc, "attn_bwd")
 
 
@@ -289,12 +305,16 @@ def block_mask_shape(Sq: int, Sk: int):
 def block_mask_document(Sq, Sk, doc_q, doc_kv, causal=False, window=0, input_pos=0):
     """Host uint8 BlockMask for DocumentMask (+ causal / window): doc_q, doc_kv are
     int32 CPU tensors of lengths Sq and Sk.  Returns a CPU uint8 tensor."""
+    Sq = _i32(Sq, "Sq")
+    Sk = _i32(Sk, "Sk")
+    window = _i32(window, "window")
+    input_pos = _i32(input_pos, "input_pos")
     out = torch.empty(block_mask_shape(Sq, Sk), dtype=torch.uint8)
     dq = doc_q.to(torch.int32).contiguous()
     dk = doc_kv.to(torch.int32).contiguous()
     assert dq.numel() == Sq and dk.numel() == Sk and not dq.is_cuda and not dk.is_cuda
-    rc = lib.attn_block_mask_document(_ptr(out), int(Sq), int(Sk), int(input_pos), int(causal),
-                                      int(window), _ptr(dq), _ptr(dk))
+    rc = lib.attn_block_mask_document(_ptr(out), Sq, Sk, input_pos, int(causal),
+                                      window, _ptr(dq), _ptr(dk))
     _check(rc, "attn_block_mask_document")
     return out
 
@@ -302,9 +322,12 @@ def block_mask_document(Sq, Sk, doc_q, doc_kv, causal=False, window=0, input_pos
 def block_mask_build(Sq, Sk, keep, input_pos=0):
     """Host uint8 BlockMask from a Python predicate keep(q, kv) -> bool on absolute
     query position q and key position kv (the page's build_block_mask)."""
+    Sq = _i32(Sq, "Sq")
+    Sk = _i32(Sk, "Sk")
+    input_pos = _i32(input_pos, "input_pos")
     out = torch.empty(block_mask_shape(Sq, Sk), dtype=torch.uint8)
     cb = _KEEP(lambda q, kv, ctx: 1 if keep(q, kv) else 0)
-    rc = lib.attn_block_mask_build(_ptr(out), int(Sq), int(Sk), int(input_pos), cb, None)
+    rc = lib.attn_block_mask_build(_ptr(out), Sq, Sk, input_pos, cb, None)
     _check(rc, "attn_block_mask_build")
     return out
 
@@ -321,8 +344,9 @@ def _check_decode(O, Q, K, V, lengths):
 
 def attn_decode(O, Q, K, V, lengths, n_splits=8, stream=None):
     """Fill O (B,Hq,D) bf16 in place; Q (B,Hq,D), K/V caches (B,Hkv,S_cap,D)."""
+    n_splits = _i32(n_splits, "n_splits")
     B, Hq, Hkv, S_cap, D = _check_decode(O, Q, K, V, lengths)
-    rc = lib.attn_decode(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(lengths), int(n_splits),
+    rc = lib.attn_decode(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(lengths), n_splits,
                          _stream(stream), B, Hq, Hkv, S_cap, D)
     _check(rc, "attn_decode")
 
@@ -330,6 +354,7 @@ def attn_decode(O, Q, K, V, lengths, n_splits=8, stream=None):
 def attn_decode_paged(O, Q, K_cache, V_cache, block_tables, seq_lens, n_splits=8, stream=None):
     """Decode from a paged cache: Q (B,Hq,D); K/V caches (num_blocks, block_size, Hkv, D);
     block_tables int32 (B, max_blocks); seq_lens int32 (B,); O (B,Hq,D) filled in place."""
+    n_splits = _i32(n_splits, "n_splits")
     B, Hq, D = _tensor(Q, "Q", torch.bfloat16, 3)
     num_blocks, block_size, Hkv, _ = _tensor(K_cache, "K_cache", torch.bfloat16,
                                              (None, None, None, D))
@@ -340,7 +365,7 @@ def attn_decode_paged(O, Q, K_cache, V_cache, block_tables, seq_lens, n_splits=8
     _same_device(O=O, Q=Q, K_cache=K_cache, V_cache=V_cache, block_tables=block_tables,
                  seq_lens=seq_lens)
     rc = lib.attn_decode_paged(_ptr(O), _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(block_tables),
-                               _ptr(seq_lens), int(n_splits), _stream(stream), B, Hq, Hkv,
+                               _ptr(seq_lens), n_splits, _stream(stream), B, Hq, Hkv,
                                num_blocks, block_size, int(block_tables.shape[1]), D)
     _check(rc, "attn_decode_paged")
 
@@ -349,9 +374,10 @@ def attn_decode_noalloc(O, Q, K, V, lengths, n_splits=8, stream=None):
     """attn_decode without any allocation: the workspace lives in the library's
     fixed 16 MiB device array (for callers that cannot allocate device memory;
     calls that overlap on the GPU share that array and must be ordered)."""
+    n_splits = _i32(n_splits, "n_splits")
     B, Hq, Hkv, S_cap, D = _check_decode(O, Q, K, V, lengths)
     rc = lib.attn_decode_noalloc(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(lengths),
-                                 int(n_splits), _stream(stream), B, Hq, Hkv, S_cap, D)
+                                 n_splits, _stream(stream), B, Hq, Hkv, S_cap, D)
     _check(rc, "attn_decode_noalloc")
 
 
@@ -359,10 +385,13 @@ def attn_fwd_sinks(O, Q, K, V, LSE, scale, window, sinks, input_pos=0, k_lengths
                    q_lengths=None, stream=None):
     """attn_fwd, causal, with a sliding window and the first ``sinks`` keys always visible:
     query position p sees keys j <= p with j > p - window or j < sinks."""
+    window = _i32(window, "window")
+    sinks = _i32(sinks, "sinks")
+    input_pos = _i32(input_pos, "input_pos")
     B, Hq, Hkv, Sq, Sk, D = _check_prefill(O, Q, K, V, LSE, k_lengths, q_lengths)
     dev = _on_device("O Q K V LSE k_lengths q_lengths", O, Q, K, V, LSE, k_lengths, q_lengths)
     rc = lib.attn_fwd_sinks(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D,
-                            float(scale), int(window), int(sinks), int(input_pos),
+                            float(scale), window, sinks, input_pos,
                             _ptr(k_lengths), _ptr(q_lengths), _stream(stream, dev))
     _check(rc, "attn_fwd_sinks")
 
@@ -370,10 +399,13 @@ def attn_fwd_sinks(O, Q, K, V, LSE, scale, window, sinks, input_pos=0, k_lengths
 def attn_bwd_sinks(dQ, dK, dV, dO, Q, K, V, O, LSE, scale, window, sinks, input_pos=0,
                    k_lengths=None, q_lengths=None, stream=None):
     """Backward of attn_fwd_sinks: fill dQ (like Q) and dK, dV (like K, V) in place."""
+    window = _i32(window, "window")
+    sinks = _i32(sinks, "sinks")
+    input_pos = _i32(input_pos, "input_pos")
     B, Hq, Hkv, Sq, Sk, D = _check_backward(dQ, dK, dV, dO, Q, K, V, O, LSE, k_lengths, q_lengths)
     rc = lib.attn_bwd_sinks(_ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V),
-                            _ptr(O), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale), int(window),
-                            int(sinks), int(input_pos), _ptr(k_lengths), _ptr(q_lengths),
+                            _ptr(O), _ptr(LSE), B, Hq, Hkv, Sq, Sk, D, float(scale), window,
+                            sinks, input_pos, _ptr(k_lengths), _ptr(q_lengths),
                             _stream(stream))
     _check(rc, "attn_bwd_sinks")
 
@@ -382,9 +414,12 @@ def attn_decode_sinks(O, Q, K, V, lengths, window, sinks, n_splits=0, stream=Non
     """attn_decode of the last cached token with a sliding window and sinks: it sees keys
     j < lengths[b] with j >= lengths[b] - window or j < sinks.  n_splits 0: the library's
     choice."""
+    window = _i32(window, "window")
+    sinks = _i32(sinks, "sinks")
+    n_splits = _i32(n_splits, "n_splits")
     B, Hq, Hkv, S_cap, D = _check_decode(O, Q, K, V, lengths)
-    rc = lib.attn_decode_sinks(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(lengths), int(window),
-                               int(sinks), int(n_splits), _stream(stream), B, Hq, Hkv, S_cap, D)
+    rc = lib.attn_decode_sinks(_ptr(O), _ptr(Q), _ptr(K), _ptr(V), _ptr(lengths), window,
+                               sinks, n_splits, _stream(stream), B, Hq, Hkv, S_cap, D)
     _check(rc, "attn_decode_sinks")
 
 
@@ -392,6 +427,9 @@ def attn_decode_paged_sinks(O, Q, K_cache, V_cache, block_tables, seq_lens, wind
                             n_splits=0, stream=None):
     """attn_decode_sinks from a paged cache; table entries of pages without a visible key
     are not read."""
+    window = _i32(window, "window")
+    sinks = _i32(sinks, "sinks")
+    n_splits = _i32(n_splits, "n_splits")
     B, Hq, D = _tensor(Q, "Q", torch.bfloat16, 3)
     _tensor(O, "O", torch.bfloat16, (B, Hq, D))
     num_blocks, block_size, Hkv, max_blocks = _check_pool(K_cache, V_cache, block_tables, B, D)
@@ -399,8 +437,8 @@ def attn_decode_paged_sinks(O, Q, K_cache, V_cache, block_tables, seq_lens, wind
     dev = _on_device("O Q K_cache V_cache block_tables seq_lens",
                      O, Q, K_cache, V_cache, block_tables, seq_lens)
     rc = lib.attn_decode_paged_sinks(_ptr(O), _ptr(Q), _ptr(K_cache), _ptr(V_cache),
-                                     _ptr(block_tables), _ptr(seq_lens), int(window), int(sinks),
-                                     int(n_splits), _stream(stream, dev), B, Hq, Hkv, num_blocks,
+                                     _ptr(block_tables), _ptr(seq_lens), window, sinks,
+                                     n_splits, _stream(stream, dev), B, Hq, Hkv, num_blocks,
                                      block_size, max_blocks, D)
     _check(rc, "attn_decode_paged_sinks")
 
@@ -494,6 +532,7 @@ def cache_fork(block_tables, ref_counts, seq_lens, parents, children, copy_src, 
                block_size, stream=None):
     """Table row children[n] continues row parents[n]: whole pages shared, a fresh page for the
     part-filled one, whose copy is left to cache_copy_blocks(copy_src, copy_dst)."""
+    block_size = _i32(block_size, "block_size")
     R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
     _tensor(seq_lens, "seq_lens", torch.int32, (R,))
     (N,) = _tensor(parents, "parents", torch.int32, 1)
@@ -505,20 +544,21 @@ def cache_fork(block_tables, ref_counts, seq_lens, parents, children, copy_src, 
     rc = lib.attn_cache_fork(_ptr(block_tables), _ptr(ref_counts), _ptr(seq_lens), _ptr(parents),
                              _ptr(children), _ptr(copy_src), _ptr(copy_dst),
                              _stream(stream, dev), N, R,
-                             num_blocks, int(block_size), max_blocks)
+                             num_blocks, block_size, max_blocks)
     _check(rc, "attn_cache_fork")
 
 
 def cache_extend(block_tables, ref_counts, from_lens, to_lens, block_size, stream=None):
     """Free pages for the empty entries of each row from the page of position from_lens[r] to
     the last page that to_lens[r] tokens need."""
+    block_size = _i32(block_size, "block_size")
     R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
     _tensor(from_lens, "from_lens", torch.int32, (R,))
     _tensor(to_lens, "to_lens", torch.int32, (R,))
     dev = _on_device("block_tables ref_counts from_lens to_lens",
                      block_tables, ref_counts, from_lens, to_lens)
     rc = lib.attn_cache_extend(_ptr(block_tables), _ptr(ref_counts), _ptr(from_lens), _ptr(to_lens),
-                               _stream(stream, dev), R, num_blocks, int(block_size), max_blocks)
+                               _stream(stream, dev), R, num_blocks, block_size, max_blocks)
     _check(rc, "attn_cache_extend")
 
 
@@ -541,4 +581,5 @@ def last_device_status(stream=None) -> int:
 
 
 def check_bounded_wait(limit_us: int, stream=None):
-    _check(lib.attn_check_bounded_wait(int(limit_us), _stream(stream)), "attn_check_bounded_wait")
+    limit_us = _i32(limit_us, "limit_us")
+    _check(lib.attn_check_bounded_wait(limit_us, _stream(stream)), "attn_check_bounded_wait")
