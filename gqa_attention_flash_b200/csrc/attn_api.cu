@@ -3,6 +3,7 @@
 // word, and the workspaces (from a per-device pool the library owns).
 #include <nvtx3/nvToolsExt.h>
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -203,6 +204,20 @@ __global__ void wait_probe_kernel(uint64_t limit_ns) {
 }
 
 }  // namespace
+
+#ifdef GQA_ATTN_DEBUG
+namespace {
+std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
+}  // namespace
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+
+// Checked build only: the bounded waits' limit in the launches that follow; negative: the
+// usual one again.
+extern "C" void attn_debug_wait_limit(long long ns) {
+    g_wait_limit_ns = ns < 0 ? kWaitLimitNs : static_cast<uint64_t>(ns);
+}
+#endif
 
 attn_status_t launch_wait_probe(int limit_us, cudaStream_t stream) {
     return launch_kernel(wait_probe_kernel, dim3(1), 32, 0, stream,

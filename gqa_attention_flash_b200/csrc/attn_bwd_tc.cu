@@ -282,7 +282,14 @@ __device__ __forceinline__ void tc_store_half(uint32_t taddr, __nv_bfloat16 *dst
     }
 }
 
-// The same columns as fp32.
+// The same columns as fp32, or zeros: what the workspace held before is never summed.
+template <int D>
+__device__ __forceinline__ void tc_zero_partial(float *dst, int c0) {
+    uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k) d4[k] = make_uint4(0, 0, 0, 0);
+}
+
 template <int D>
 __device__ __forceinline__ void tc_store_partial(uint32_t taddr, float *dst, int c0) {
 #pragma unroll
@@ -617,11 +624,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                           warp_wait(bar(C::BAR_DONE), 0, abort_flag, p.wait_limit_ns, p.status);
         const long long krow = (long long)(b * p.Hkv + hkv) * p.Sk + j;
         if (kSink && split > 1) {
+            float *dst = p.part + (long long)blockIdx.x * (2 * TB * D) + r * D;
             if (have) {
                 tc_fence_after();
-                float *dst = p.part + (long long)blockIdx.x * (2 * TB * D) + r * D;
                 tc_store_partial<D>(trow + C::COL_A, dst, half * (D / 2));
                 tc_store_partial<D>(trow + C::COL_B, dst + TB * D, half * (D / 2));
+            } else {  // no item, or a bounded wait ran out
+                tc_zero_partial<D>(dst, half * (D / 2));
+                tc_zero_partial<D>(dst + TB * D, half * (D / 2));
             }
         } else if (have) {
             tc_fence_after();
@@ -1046,7 +1056,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     p.window = a.window;
     p.input_pos = a.input_pos;
     p.sinks = a.sinks;
-    p.wait_limit_ns = kWaitLimitNs;
+    p.wait_limit_ns = wait_limit_ns();
     p.status = device_status_word();
     if (!p.status) return ATTN_ERR_CUDA;
     const int n_qt = (a.Sq + TB - 1) / TB;

@@ -636,7 +636,7 @@ attn_status_t launch_decode_d(const DecodeArgs &a, cudaStream_t stream) {
     p.group = a.Hq / a.Hkv;
     p.n_splits = a.n_splits;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-    p.wait_limit_ns = kWaitLimitNs;
+    p.wait_limit_ns = wait_limit_ns();
     p.status = device_status_word();
     if (!p.status) return ATTN_ERR_CUDA;
     p.block_tables = a.block_tables;

@@ -1040,7 +1040,7 @@ attn_status_t launch_fwd_d(const FwdArgs &a, cudaStream_t stream) {
     p.window = a.window;
     p.input_pos = a.input_pos;
     p.sinks = a.sinks;
-    p.wait_limit_ns = kWaitLimitNs;
+    p.wait_limit_ns = wait_limit_ns();
     p.status = device_status_word();
     p.scale = a.scale;
     p.softcap = a.softcap;

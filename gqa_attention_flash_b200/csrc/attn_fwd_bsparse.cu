@@ -494,7 +494,7 @@ attn_status_t launch_bsparse_d(const FwdArgs &a, cudaStream_t stream) {
     p.n_qb = (a.Sq + 63) / 64;
     p.n_kb = (a.Sk + 63) / 64;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.wait_limit_ns = kWaitLimitNs;
+    p.wait_limit_ns = wait_limit_ns();
     p.status = device_status_word();
     if (!p.status) return ATTN_ERR_CUDA;
     const long long grid = (long long)p.n_qt * a.Hq * a.B;

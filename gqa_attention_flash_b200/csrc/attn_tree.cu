@@ -800,7 +800,7 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
     while ((1 << p.shift) < a.block_size) ++p.shift;
     p.box_rows = a.block_size < TK ? a.block_size : TK;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-    p.wait_limit_ns = kWaitLimitNs;
+    p.wait_limit_ns = wait_limit_ns();
     p.status = device_status_word();
     if (!p.status) return ATTN_ERR_CUDA;
     int dev = 0, n_sm = 0;

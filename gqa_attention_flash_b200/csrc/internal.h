@@ -202,4 +202,13 @@ cudaError_t kernel_setup(const void *func, int smem_bytes, int required_regs = -
 // Bounded-wait limit used by the attention kernels (nanoseconds of global time).
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
+// The limit of the next launches: kWaitLimitNs.  The checked build's tests set another with
+// attn_debug_wait_limit; with 0 every wait gives up at once, which shows what a kernel
+// leaves behind then.
+#ifdef GQA_ATTN_DEBUG
+uint64_t wait_limit_ns();
+#else
+constexpr uint64_t wait_limit_ns() { return kWaitLimitNs; }
+#endif
+
 }  // namespace gqa

@@ -101,6 +101,11 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 // issuing work and head for the exit path".
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                           uint64_t limit_ns, int *status) {
+    if (kChecked && limit_ns == 0) {
+        *abort_flag = 1;
+        record_status(status, ATTN_ERR_TIMEOUT);
+        return false;
+    }
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1;; ++it) {
