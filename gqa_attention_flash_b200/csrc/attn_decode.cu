@@ -508,18 +508,20 @@ __global__ void __launch_bounds__(kDecThreads)
                         if (d == 0) dst[D] = (M + __log2f(lsum)) * 0.69314718055994531f;
                     }
                 }
-            } else {
-                // A bounded wait ran out: the slice weighs nothing in the combine, so
-                // whatever the workspace held before (another call's partials) never
-                // reaches O.
-                for (int h = threadIdx.x; h < G && ws_ok; h += 32 * kConsumers) {
-                    if constexpr (kCluster) part[G * D + h] = neg_inf();
-                    else ws_base[h * ws_head + D] = neg_inf();
-                }
             }
         }
         if (*abort_flag) drain_delay(2000000);
         __syncthreads();
+        if (*abort_flag) {
+            // A bounded wait ran out: the slice weighs nothing in the combine, so whatever
+            // the workspace held before (another call's partials) never reaches O.  Marked
+            // only here: the partials of a cluster stand in the ring, where copies were in
+            // flight until now, and no thread writes a result after the others' mark.
+            for (int h = threadIdx.x; h < G && ws_ok; h += kDecThreads) {
+                if constexpr (kCluster) part[G * D + h] = neg_inf();
+                else ws_base[h * ws_head + D] = neg_inf();
+            }
+        }
     }
     if constexpr (kCluster) {
         // one slice: written above, unless it has no key (or a bounded wait ran out)
