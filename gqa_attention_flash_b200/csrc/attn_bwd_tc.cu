@@ -35,7 +35,7 @@
 // kernels are independent: dQ runs on a library-owned side stream forked from and
 // joined back to the caller's stream with events, so each kernel's last wave
 // overlaps the other's work (3 % on the LLM causal backward, bitwise the same).
-// The side stream and its events are shared per device; a mutex keeps the
+// The side streams and their events are shared per device; a mutex keeps the
 // fork / launch / join sequence of concurrent callers from interleaving.  Key,
 // value, query and output-gradient rows past the lengths are read as MMA
 // operands with weight exactly zero, so they must hold finite values: zero times
@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 
 #include <mutex>
+#include <vector>
 
 #include "internal.h"
 #include "sm100_ptx.cuh"
@@ -982,26 +983,47 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 struct SideStream {
     cudaStream_t s = nullptr;
     cudaEvent_t fork = nullptr, join = nullptr;
-    std::mutex mu;
 };
 
-// One side stream (and its fork / join events) per device, made on first use.
-SideStream *side_stream() {
-    static std::mutex mu;
-    static SideStream *per_dev[64] = {};
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!per_dev[dev]) {
-        SideStream *ss = new SideStream();
-        if (cudaStreamCreateWithFlags(&ss->s, cudaStreamNonBlocking) != cudaSuccess ||
-            cudaEventCreateWithFlags(&ss->fork, cudaEventDisableTiming) != cudaSuccess ||
-            cudaEventCreateWithFlags(&ss->join, cudaEventDisableTiming) != cudaSuccess)
+// Side streams of each device (with their fork / join events), made when needed.  A side
+// stream forked from a stream that is being captured belongs to that capture until it ends,
+// and a call of another stream meanwhile may not touch it; so a call takes one that belongs to
+// its own capture, or to none.  The caller holds `mu` from here to its join.
+struct SideStreams {
+    std::mutex mu;
+    std::vector<SideStream> all[64];
+
+    SideStream *get(cudaStream_t caller) {
+        int dev = -1;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+        cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+        unsigned long long id = 0;
+        if (cudaStreamGetCaptureInfo(caller, &st, &id) != cudaSuccess) return nullptr;
+        SideStream *found = nullptr;
+        for (SideStream &x : all[dev]) {
+            cudaStreamCaptureStatus xs = cudaStreamCaptureStatusNone;
+            unsigned long long xid = 0;
+            if (cudaStreamGetCaptureInfo(x.s, &xs, &xid) != cudaSuccess) return nullptr;
+            if (xs == cudaStreamCaptureStatusNone) {
+                if (!found) found = &x;
+            } else if (st == cudaStreamCaptureStatusActive && xs == st && xid == id) {
+                return &x;
+            }
+        }
+        if (found) return found;
+        SideStream x;
+        if (cudaStreamCreateWithFlags(&x.s, cudaStreamNonBlocking) != cudaSuccess) return nullptr;
+        if (cudaEventCreateWithFlags(&x.fork, cudaEventDisableTiming) != cudaSuccess ||
+            cudaEventCreateWithFlags(&x.join, cudaEventDisableTiming) != cudaSuccess) {
+            if (x.fork) cudaEventDestroy(x.fork);
+            cudaStreamDestroy(x.s);
             return nullptr;
-        per_dev[dev] = ss;
+        }
+        all[dev].push_back(x);
+        return &all[dev].back();
     }
-    return per_dev[dev];
-}
+};
+SideStreams g_side;
 
 // Stream-ordered workspace, given back on every way out.
 struct Workspace {
@@ -1136,9 +1158,9 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
         return launch_dq(stream) && launch_dkdv() && part.release() ? ATTN_OK : ATTN_ERR_CUDA;
     // dK/dV and dQ are independent: run dQ on a side stream so that each kernel's
     // last wave overlaps the other's work.
-    SideStream *ss = side_stream();
+    std::lock_guard<std::mutex> lock(g_side.mu);
+    SideStream *ss = g_side.get(stream);
     if (!ss) return ATTN_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(ss->mu);
     if (cudaEventRecord(ss->fork, stream) != cudaSuccess ||
         cudaStreamWaitEvent(ss->s, ss->fork, 0) != cudaSuccess)
         return ATTN_ERR_CUDA;

@@ -128,6 +128,13 @@ cudaError_t cudaEventCreateWithFlags(cudaEvent_t *e, unsigned) {
     *e = static_cast<cudaEvent_t>(handle());
     return fails() ? cudaErrorUnknown : cudaSuccess;
 }
+cudaError_t cudaStreamGetCaptureInfo_v2(cudaStream_t, cudaStreamCaptureStatus *st, unsigned long long *,
+                                        cudaGraph_t *, const cudaGraphNode_t **, size_t *) {
+    *st = cudaStreamCaptureStatusNone;
+    return fails() ? cudaErrorUnknown : cudaSuccess;
+}
+cudaError_t cudaEventDestroy(cudaEvent_t) { return cudaSuccess; }
+cudaError_t cudaStreamDestroy(cudaStream_t) { return cudaSuccess; }
 cudaError_t cudaEventRecord(cudaEvent_t e, cudaStream_t s) {
     if (fails()) return cudaErrorUnknown;
     note(kRecord, s, e);
