@@ -68,6 +68,17 @@ cudaError_t kernel_setup(const void *func, int smem_bytes, int required_regs, bo
 }
 
 namespace {
+// While a stream is captured in the global mode (or by this thread), the runtime refuses
+// allocations on other streams and spoils the capture, since an allocation may synchronise.
+// Stream-ordered ones do not: for their time the thread has the relaxed mode.
+struct AnyCaptureMode {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    AnyCaptureMode() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~AnyCaptureMode() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
+    AnyCaptureMode(const AnyCaptureMode &) = delete;
+    AnyCaptureMode &operator=(const AnyCaptureMode &) = delete;
+};
+
 std::mutex g_pool_mutex;
 cudaMemPool_t g_pool[64] = {};
 bool g_pool_made[64] = {};
@@ -101,7 +112,13 @@ cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream) {
         }
         pool = g_pool[dev];
     }
+    AnyCaptureMode any;
     return cudaMallocFromPoolAsync(ptr, bytes, pool, stream);
+}
+
+cudaError_t workspace_free(void *ptr, cudaStream_t stream) {
+    AnyCaptureMode any;
+    return cudaFreeAsync(ptr, stream);
 }
 
 namespace {
@@ -444,7 +461,7 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
     a.window = window;
     a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
-    if (needs_ws && cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (needs_ws && workspace_free(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return answer(st);
 }
 
@@ -536,7 +553,7 @@ attn_status_t backward(void *dQ, void *dK, void *dV, const void *dO, const void 
     a.sinks = sinks;
     a.delta = static_cast<float *>(ws);
     st = launch_bwd(a, s);
-    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (workspace_free(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return answer(st);
 }
 
@@ -603,7 +620,7 @@ attn_status_t attn_rbs_block_mask(uint8_t *block_mask, float *base_scores, float
     a.rad = a.cent + (size_t)B * Hkv * nkb * D;
     a.beta = a.rad + (size_t)B * Hkv * nkb;
     attn_status_t st = launch_rbs(a, s);
-    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (workspace_free(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return answer(st);
 }
 
@@ -655,7 +672,7 @@ attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const vo
     a.window = window;
     a.sinks = sinks;
     attn_status_t st = launch_decode(a, s);
-    if (needs_ws && cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (needs_ws && workspace_free(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return answer(st);
 }
 
@@ -850,7 +867,7 @@ attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_
     a.max_blocks = max_blocks_per_seq;
     a.workspace = static_cast<int32_t *>(ws);
     st = launch_cache_fork(a, s);
-    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (workspace_free(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return answer(st);
 }
 
@@ -883,7 +900,7 @@ attn_status_t attn_cache_extend(int32_t *block_tables, int32_t *ref_counts, cons
     a.max_blocks = max_blocks_per_seq;
     a.workspace = static_cast<int32_t *>(ws);
     st = launch_cache_extend(a, s);
-    if (cudaFreeAsync(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (workspace_free(ws, s) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return answer(st);
 }
 

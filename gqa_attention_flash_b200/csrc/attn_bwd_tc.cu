@@ -1041,7 +1041,7 @@ struct Workspace {
     bool release() {
         void *p = ptr;
         ptr = nullptr;
-        return !p || cudaFreeAsync(p, stream) == cudaSuccess;
+        return !p || workspace_free(p, stream) == cudaSuccess;
     }
 };
 

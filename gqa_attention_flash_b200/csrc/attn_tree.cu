@@ -854,7 +854,7 @@ attn_status_t launch_tree_d(const TreeArgs &a, cudaStream_t stream,
         if (cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, C>, p, row_blocks, rows_per_block) != cudaSuccess)
             st = ATTN_ERR_CUDA;
     }
-    if (cudaFreeAsync(ws, stream) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
+    if (workspace_free(ws, stream) != cudaSuccess && st == ATTN_OK) st = ATTN_ERR_CUDA;
     return st;
 }
 

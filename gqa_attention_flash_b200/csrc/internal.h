@@ -31,9 +31,10 @@ attn_status_t make_tmap_bf16_paged_wide(CUtensorMap *map, const void *base, uint
 attn_status_t make_tmap_bf16_paged_groups(CUtensorMap *map, const void *base, uint64_t D, uint64_t heads,
                                           uint64_t rows, uint32_t box_rows);
 
-// Stream-ordered workspace from the library's pool on the current device (freed with
-// cudaFreeAsync on the same stream).
+// Stream-ordered workspace from the library's pool on the current device, and its end on the
+// same stream.
 cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream);
+cudaError_t workspace_free(void *ptr, cudaStream_t stream);
 
 // What an entry point answers.  A CUDA call that failed also leaves its error with the
 // runtime, where the process's next check of it, in whatever code, would take it for its

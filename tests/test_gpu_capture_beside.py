@@ -72,7 +72,7 @@ class Graph:
         assert self.rt.cudaGraphDestroy(self.graph) == 0
 
 
-@pytest.mark.parametrize("mode", [2])  # relaxed
+@pytest.mark.parametrize("mode", [0, 1, 2])  # global, thread-local, relaxed
 @pytest.mark.parametrize("sinks", [False, True])
 def test_eager_beside_a_capture(sinks, mode):
     a, b = Backward(0, sinks), Backward(10, sinks)
@@ -93,6 +93,48 @@ def test_eager_beside_a_capture(sinks, mode):
         b(sb)
     a.check()
     b.check()
+    g.free()
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+def test_workspaces_beside_a_capture(mode):
+    """Calls on another stream that allocate: decode in slices, a tree, fork and extend."""
+    q, k = rand(0, 2, 8, D), rand(1, 40, 16, 2, D)
+    o, O = torch.empty_like(q), torch.empty((2, 8, 3, D), dtype=BF, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, par = i32([100, 37]), i32([[-1, 0, 1]] * 2)
+    t0, refs0 = torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10), torch.zeros(40, dtype=torch.int32, device="cuda")
+    t, refs, L, p, c, src, dst = t0.clone(), refs0.clone(), lens.clone(), i32([0]), i32([1]), i32([0]), i32([0])
+    to, Q3 = L + 60, rand(2, 2, 8, 3, D)
+
+    def calls(s):
+        binding.attn_decode_paged(o, q, k, k, t0, lens, 8, stream=s)
+        binding.attn_tree_paged(O, Q3, k, k, t0, lens, par, stream=s)
+        binding.cache_fork(t, refs, L, p, c, src, dst, 16, stream=s)
+        binding.cache_extend(t, refs, L, to, 16, stream=s)
+
+    def result():
+        torch.cuda.synchronize()
+        assert binding.last_device_status() == 0
+        got = [x.clone() for x in (o, O, t, refs, L, src, dst)]
+        for x, y in ((t, t0), (refs, refs0), (L, lens)):
+            x.copy_(y)
+        o.zero_(), O.zero_()
+        torch.cuda.synchronize()
+        return got
+
+    calls(None)
+    want = result()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    g = Graph(sa, mode)
+    try:
+        calls(sa)
+        calls(sb)
+    finally:
+        g.end()
+    assert all(torch.equal(x, y) for x, y in zip(result(), want))
+    g.launch()
+    assert all(torch.equal(x, y) for x, y in zip(result(), want))
     g.free()
 
 
