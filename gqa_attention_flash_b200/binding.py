@@ -531,7 +531,9 @@ def _check_table(block_tables, ref_counts):
 def cache_fork(block_tables, ref_counts, seq_lens, parents, children, copy_src, copy_dst,
                block_size, stream=None):
     """Table row children[n] continues row parents[n]: whole pages shared, a fresh page for the
-    part-filled one, whose copy is left to cache_copy_blocks(copy_src, copy_dst)."""
+    part-filled one, whose copy is left to cache_copy_blocks(copy_src, copy_dst).  A child for
+    which there was no page (ATTN_ERR_NO_PAGES) has a negative entry at seq_lens // block_size:
+    free its row and fork it again, never extend it."""
     block_size = _i32(block_size, "block_size")
     R, max_blocks, num_blocks = _check_table(block_tables, ref_counts)
     _tensor(seq_lens, "seq_lens", torch.int32, (R,))

@@ -369,6 +369,13 @@ __global__ void __launch_bounds__(kTableThreads) fork_kernel(const ForkParams p)
 // ---------------------------------------------------------------------------------
 constexpr int kAllocThreads = 1024;
 
+// No page left.  A length out of range that was recorded before (a clamp) does not hide it:
+// the caller has to act on missing pages.
+__device__ __forceinline__ void record_no_pages(int *status) {
+    if (atomicCAS(status, 0, ATTN_ERR_NO_PAGES) == ATTN_ERR_DEVICE_BOUNDS)
+        atomicCAS(status, ATTN_ERR_DEVICE_BOUNDS, ATTN_ERR_NO_PAGES);
+}
+
 // Exclusive sum over the block; `total` gets the whole sum.
 __device__ __forceinline__ int block_exclusive(int v, int *warp_sums, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(kAllocThreads) fork_alloc_kernel(const ForkPar
         need += total;
     }
     const int got = free_pages(p.refs, p.num_blocks, need, list, warp_sums);
-    if (got < need && threadIdx.x == 0) record_status(p.status, ATTN_ERR_NO_PAGES);
+    if (got < need && threadIdx.x == 0) record_no_pages(p.status);
     int before = 0;
     for (int n0 = 0; n0 < p.N; n0 += kAllocThreads) {
         const int n = n0 + threadIdx.x;
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kAllocThreads) extend_kernel(const ExtendParam
     const int need = static_cast<int>(min(need_all, (long long)p.num_blocks));
     if (need == 0) return;
     const int got = free_pages(p.refs, p.num_blocks, need, p.list, warp_sums);
-    if (got < need_all && threadIdx.x == 0) record_status(p.status, ATTN_ERR_NO_PAGES);
+    if (got < need_all && threadIdx.x == 0) record_no_pages(p.status);
     for (int r = warp; r < p.R; r += kAllocThreads / 32) {
         int k0, k1;
         extend_range(p, r, false, k0, k1);

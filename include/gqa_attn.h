@@ -439,7 +439,8 @@ attn_status_t attn_cache_compact(void *K_cache, void *V_cache, const int32_t *bl
  * attn_cache_copy_blocks -- page dst[i] takes the contents of page src[i], i < N, in both
  * pools.  A pair with a negative entry is no pair.  A pair is skipped and flagged
  * ATTN_ERR_DEVICE_BOUNDS when a page is outside the pool, when its source is another
- * pair's destination, or when a later pair names the same destination.  N <= 65536.
+ * pair's destination, or when a later pair names the same destination.  N <= 65536; every
+ * pair is compared with all others, so a list of tens of thousands costs milliseconds.
  */
 attn_status_t attn_cache_copy_blocks(void *K_cache, void *V_cache, const int32_t *src,
                                      const int32_t *dst, void *stream, int N, int num_blocks,
@@ -459,7 +460,14 @@ attn_status_t attn_cache_copy_blocks(void *K_cache, void *V_cache, const int32_t
  * with a negative entry is no pair.  A pair is skipped and flagged ATTN_ERR_DEVICE_BOUNDS
  * when a row is outside the table, when its child is also a parent, or the child of an
  * earlier pair.  Free pages go to the pairs in order; a pair that gets none keeps -1
- * there and the call flags ATTN_ERR_NO_PAGES.  N <= 65536.
+ * there and the call flags ATTN_ERR_NO_PAGES (also over a DEVICE_BOUNDS that no one has
+ * read yet).  N <= 65536; every pair is compared with all others.
+ * A child without its last page is the one whose seq_lens is not a multiple of block_size
+ * and whose table entry at seq_lens / block_size is negative (its copy_src and copy_dst
+ * are -1).  Its last tokens are nowhere: attention flags the missing page, but
+ * attn_cache_extend would put an empty page there and its old rows would be read.  Free
+ * its row and fork it again when there are pages.  Entries that the parent itself lacks
+ * are missing in the child too, without a flag.
  */
 attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_t *seq_lens,
                               const int32_t *parents, const int32_t *children,
@@ -472,7 +480,8 @@ attn_status_t attn_cache_fork(int32_t *block_tables, int32_t *ref_counts, int32_
  * need get free pages (count 1), rows in order, entries in order.  Entries that hold a
  * page keep it.  to_lens[r] past the table is clamped and flagged
  * ATTN_ERR_DEVICE_BOUNDS; entries for which no page is left stay as they are and the call
- * flags ATTN_ERR_NO_PAGES.
+ * flags ATTN_ERR_NO_PAGES (over DEVICE_BOUNDS, as fork).  A page comes with the rows that it
+ * held before; the caller writes those that it reads (attn_cache_append).
  *   block_tables, ref_counts [in/out], from_lens, to_lens [in] int32 (R,).
  * R * max_blocks_per_seq is below 2^31.
  */
@@ -498,7 +507,8 @@ const char *attn_status_string(attn_status_t status);
 /*
  * attn_last_device_status -- synchronise `stream`, then return and clear the
  * status word that kernels of this library set on the current device
- * (ATTN_OK if none did).  Returns ATTN_ERR_CUDA if the synchronisation failed.
+ * (ATTN_OK if none did).  The word keeps the first status set since it was last
+ * read, except that ATTN_ERR_NO_PAGES replaces ATTN_ERR_DEVICE_BOUNDS.  Returns ATTN_ERR_CUDA if the synchronisation failed.
  */
 attn_status_t attn_last_device_status(void *stream);
 
