@@ -15,8 +15,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libgqa_attn.so")
-# Checked build: every TMA coordinate and global index is range-checked in the
-# kernels (a violation sets ATTN_ERR_DEVICE_BOUNDS and the kernel gives up).
+# Checked build: TMA coordinates, workspace slots, table entries and pool rows are
+# range-checked in the kernels (a violation sets ATTN_ERR_DEVICE_BOUNDS and the access is
+# skipped).
 DEBUG_LIBRARY = os.path.join(PKG, "libgqa_attn_debug.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -101,6 +101,7 @@ struct TcParams {
     // partials of split tiles, a slot per CTA
     int sinks, sink_tiles, split_sink, split_win;
     float *part;
+    long long slots;  // of `part`
     uint64_t wait_limit_ns;
     int *status;
 };
@@ -625,12 +626,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                           warp_wait(bar(C::BAR_DONE), 0, abort_flag, p.wait_limit_ns, p.status);
         const long long krow = (long long)(b * p.Hkv + hkv) * p.Sk + j;
         if (kSink && split > 1) {
+            // checked build: the CTA has a slot of the workspace
+            const bool slot_ok = in_range(blockIdx.x < p.slots, p.status, abort_flag);
             float *dst = p.part + (long long)blockIdx.x * (2 * TB * D) + r * D;
-            if (have) {
+            if (have && slot_ok) {
                 tc_fence_after();
                 tc_store_partial<D>(trow + C::COL_A, dst, half * (D / 2));
                 tc_store_partial<D>(trow + C::COL_B, dst + TB * D, half * (D / 2));
-            } else {  // no item, or a bounded wait ran out
+            } else if (slot_ok) {  // no item, or a bounded wait ran out
                 tc_zero_partial<D>(dst, half * (D / 2));
                 tc_zero_partial<D>(dst + TB * D, half * (D / 2));
             }
@@ -685,6 +688,8 @@ __global__ void __launch_bounds__(256) bwd_dkdv_reduce_kernel(const TcParams p) 
         const int which = x / (kRows * kVec), r = blockIdx.y * kRows + x / kVec % kRows, c = x % kVec;
         const int j = kv0 + r;
         if (j >= p.Sk) continue;
+        // checked build: the tile's parts stand in the workspace, its rows in dK and dV
+        if (!in_range(slot + parts <= p.slots && pair < pairs && kt >= 0, p.status, nullptr)) continue;
         float acc[8] = {};
         const float *src = p.part + ((long long)slot * 2 + which) * (TB * D) + r * D + c * 8;
 #pragma unroll 4
@@ -1088,6 +1093,7 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
     long long grid_kv = (long long)n_kt * pairs, reduce = 0;
     Workspace part(stream);
     p.part = nullptr;
+    p.slots = 0;
     p.sink_tiles = 0;
     p.split_sink = p.split_win = 1;
     int n_sm = 148;
@@ -1117,8 +1123,8 @@ attn_status_t launch_bwd_tc_d(const BwdArgs &a, cudaStream_t stream) {
         if (p.split_sink > 1) reduce += (long long)p.sink_tiles * pairs;
         if (p.split_win > 1) reduce += others;
         if (reduce > 0) {
-            const long long slots = p.split_win > 1 ? grid_kv : sink_ctas;
-            if (!part.alloc((size_t)slots * 2 * TB * D * sizeof(float))) return ATTN_ERR_CUDA;
+            p.slots = p.split_win > 1 ? grid_kv : sink_ctas;
+            if (!part.alloc((size_t)p.slots * 2 * TB * D * sizeof(float))) return ATTN_ERR_CUDA;
             p.part = static_cast<float *>(part.ptr);
         }
     }

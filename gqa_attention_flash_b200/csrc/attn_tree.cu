@@ -93,6 +93,11 @@ struct TreeParams {
     // sequence; a lane's list of segs segments per sequence is cut into n_run runs, run k
     // of lane l being CTA k * lanes + l
     int lanes, segs, n_run;
+    // checked build: the n-th partial is one of the workspace's; `row` is one of O's
+    __device__ __forceinline__ bool slot_ok(long long n) const { return n >= 0 && n < 2ll * lanes * n_run; }
+    __device__ __forceinline__ bool row_ok(long long row) const {
+        return row >= 0 && row < (long long)B * Hq * T;
+    }
     float scale_log2;
     uint64_t wait_limit_ns;
     int *status;
@@ -303,7 +308,11 @@ __device__ __forceinline__ void tree_produce(const TreeParams &p, uint8_t *smem,
         // page of this lane's chunk, read one tile ahead
         auto page_of = [&](int tile) -> int {
             const long long j = (long long)tile * TK + lane * p.box_rows;
-            return lane * p.box_rows < TK && j < n_keys ? bt[j >> p.shift] : -1;
+            // checked build: the entry is one of the sequence's
+            return lane * p.box_rows < TK && j < n_keys &&
+                           in_range((j >> p.shift) < p.max_blocks, p.status, abort_flag)
+                       ? bt[j >> p.shift]
+                       : -1;
         };
         const int n = w.t_b - w.t_a;
         int page = page_of(w.t_a);
@@ -340,6 +349,11 @@ __device__ __forceinline__ void tree_produce(const TreeParams &p, uint8_t *smem,
                 if (piece > 0 && !mbar_wait(bar(C::BAR_QFREE), (piece - 1) & 1, abort_flag, p.wait_limit_ns,
                                             p.status)) {
                     ok = false;
+                } else if (!in_range(box_ok(0, w.rt * C::ROWS, w.b * p.Hkv + w.hkv, D, p.R,
+                                            (long long)p.B * p.Hkv, C::RQ) &&
+                                         w.rt * C::ROWS < p.R,
+                                     p.status, abort_flag)) {
+                    ok = false;  // checked build: the head's rows are not Q's
                 } else {
                     const int n_q = C::NQ == 2 && tree_rows<C>(p, w.rt, 1) > 0 ? 2 : 1;
                     mbar_arrive_expect_tx(bar(C::BAR_QFULL), n_q * C::QTILE);
@@ -470,6 +484,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (n_iter > 0 && (long long)w.t_b * TK > ctx) {
                 // the tree: a parent per draft, 255 = the context
                 for (int i = r; i < w.len.drafts; i += TM) {
+                    // checked build: the parent is one of the sequence's
+                    if (!in_range(w.b < p.B && i < p.T, p.status, abort_flag)) break;
                     const int up = p.parents[(long long)w.b * p.T + i];
                     const bool good = up >= -1 && up < i;
                     if (!good) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
@@ -636,11 +652,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 c_lo = t * (D / 64);
                 c_hi = c_lo + D / 64;
             }
-            const bool write = row < p.R && (!kTwo || n_iter > 0);
+            bool write = row < p.R && (!kTwo || n_iter > 0);
             const bool use1 = !kTwo && n > 1, zero = a0 < 0.f;
             const long long orow = (long long)(w.b * p.Hq + w.hkv * (p.Hq / p.Hkv)) * p.T + row;
             float *part = p.ws + (long long)w.slot(blockIdx.x) * C::WS;
             const int prow = (kTwo ? t * TM : 0) + r;
+            // checked build: the row is one of O's, the partial one of the workspace's
+            if (write)
+                write = in_range(whole ? p.row_ok(orow) : p.slot_ok(w.slot(blockIdx.x)) && prow < C::ROWS,
+                                 p.status, abort_flag);
             tc_fence_after();
             if (have_rows && (!kTwo || n_iter > 0)) {
                 for (int c = c_lo; c < c_hi; ++c) {
@@ -721,6 +741,10 @@ __global__ void __launch_bounds__(kCombineThreads)
     for (int k = warp; k < rows_per_block; k += kCombineThreads / 32) {
         const int row = rb * rows_per_block + k;
         if (row >= p.R) break;
+        // checked build: the row is one of O's
+        if (!in_range(b < p.B && p.row_ok((long long)(b * p.Hq + hkv * (p.Hq / p.Hkv)) * p.T + row), p.status,
+                      nullptr))
+            break;
         __nv_bfloat16 *out = p.O + ((long long)(b * p.Hq + hkv * (p.Hq / p.Hkv)) * p.T + row) * D + lane * PER;
         float acc[PER] = {};
         float inv = 0.f;
@@ -736,6 +760,11 @@ __global__ void __launch_bounds__(kCombineThreads)
             auto piece = [&](int i) -> const float * {
                 return p.ws + (2 * ((long long)(c0 + i) * p.lanes + lane_q) + (i == 0 ? odd : 0)) * C::WS;
             };
+            // checked build: all pieces stand in the workspace
+            if (!in_range(p.slot_ok(2 * ((long long)c0 * p.lanes + lane_q) + odd) &&
+                              p.slot_ok(2 * ((long long)(c0 + n - 1) * p.lanes + lane_q)) && prow < C::ROWS,
+                          p.status, nullptr))
+                continue;
             float M = ninf(), lsum = 0.f;
             for (int i0 = 0; i0 < n; i0 += 32) {
                 const bool has = i0 + lane < n;

@@ -42,7 +42,11 @@ attn_status_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_
 
 // Pool row of position `pos` of the sequence whose table row is `bt`, or -1 (no page,
 // or a page outside the pool).
-__device__ __forceinline__ long long pool_row(const int32_t *bt, int pos, int shift, int num_blocks) {
+template <class Params>
+__device__ __forceinline__ long long pool_row(const Params &q, const int32_t *bt, int pos) {
+    const int shift = q.shift, num_blocks = q.num_blocks;
+    // checked build: the entry lies in the sequence's table row
+    if (!in_range(pos >= 0 && (pos >> shift) < q.max_blocks, q.status, nullptr)) return -1;
     const int p = bt[pos >> shift];
     return p >= 0 && p < num_blocks ? ((long long)p << shift) + (pos & ((1 << shift) - 1)) : -1;
 }
@@ -60,7 +64,7 @@ struct AppendParams {
     uint4 *K, *V;
     const uint4 *Kn, *Vn;
     const int32_t *tables, *start, *n_new;
-    int Hkv, T, vec, max_blocks, shift, num_blocks, chunks;  // vec: 16-byte words per head row
+    int B, Hkv, T, vec, max_blocks, shift, num_blocks, chunks;  // vec: 16-byte words per head row
     long long capacity;
     int *status;
 };
@@ -91,15 +95,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
         if (t >= n) continue;
         const long long pos = start + t;
         long long row = -1;
-        if (pos >= 0 && pos < p.capacity) row = pool_row(bt, static_cast<int>(pos), p.shift, p.num_blocks);
+        if (pos >= 0 && pos < p.capacity) row = pool_row(p, bt, static_cast<int>(pos));
         if (row < 0) {
             record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
             continue;
         }
-        const long long src = (bh * p.T + t) * p.vec + c;
+        const long long src = (bh * p.T + t) * p.vec + c, to = (row * p.Hkv + h) * p.vec + c;
+        // checked build: both rows lie inside their tensors
+        if (!in_range(t < p.T && src < (long long)p.B * p.Hkv * p.T * p.vec &&
+                          to < ((long long)p.num_blocks << p.shift) * p.Hkv * p.vec,
+                      p.status, nullptr))
+            continue;
         k[u] = p.Kn[src];
         v[u] = p.Vn[src];
-        dst[u] = (row * p.Hkv + h) * p.vec + c;
+        dst[u] = to;
     }
 #pragma unroll
     for (int u = 0; u < kAppendUnroll; ++u)
@@ -171,9 +180,8 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
             // (an entry that passes has k <= x, so both positions lie in the table)
             const bool fits = base >= 0 && x[i] > before[i] && x[i] >= k && base + x[i] < p.capacity;
             const long long from =
-                fits ? pool_row(bt, static_cast<int>(base + x[i]), p.shift, p.num_blocks) : -1;
-            const long long to =
-                fits ? pool_row(bt, static_cast<int>(base + k), p.shift, p.num_blocks) : -1;
+                fits ? pool_row(p, bt, static_cast<int>(base + x[i])) : -1;
+            const long long to = fits ? pool_row(p, bt, static_cast<int>(base + k)) : -1;
             bad = bad || from < 0 || to < 0;
             if (k < kCompactList) {
                 rows_from[k] = static_cast<int>(from);
@@ -191,25 +199,29 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
         const int m = min(n - l0, kCompactList);  // rows l0 .. l0 + m - 1 of the list
         if (l0 > 0) __syncthreads();  // the first rows are there from the check
         for (int k = threadIdx.x; k < m && l0 > 0; k += kCompactThreads) {
-            rows_from[k] = static_cast<int>(
-                pool_row(bt, static_cast<int>(base + keep[l0 + k]), p.shift, p.num_blocks));
-            rows_to[k] =
-                static_cast<int>(pool_row(bt, static_cast<int>(base + l0 + k), p.shift, p.num_blocks));
+            rows_from[k] = static_cast<int>(pool_row(p, bt, static_cast<int>(base + keep[l0 + k])));
+            rows_to[k] = static_cast<int>(pool_row(p, bt, static_cast<int>(base + l0 + k)));
         }
         if (l0 > 0) __syncthreads();
         uint4 v[2][kPasses];
+        // checked build: row k of the list is one of the pool's
+        auto ok = [&](const int *rows, int k) -> bool {
+            return in_range(k < kCompactList && rows[k] >= 0 &&
+                                rows[k] < ((long long)p.num_blocks << p.shift),
+                            p.status, nullptr);
+        };
         auto read = [&](uint4 (&x)[kPasses], int k0) {
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int k = k0 + i * kStepRows + r;
-                if (k < m && col < p.row_vec) x[i] = pool[(long long)rows_from[k] * p.row_vec + col];
+                if (k < m && col < p.row_vec && ok(rows_from, k)) x[i] = pool[(long long)rows_from[k] * p.row_vec + col];
             }
         };
         auto write = [&](const uint4 (&x)[kPasses], int k0) {
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int k = k0 + i * kStepRows + r;
-                if (k < m && col < p.row_vec) pool[(long long)rows_to[k] * p.row_vec + col] = x[i];
+                if (k < m && col < p.row_vec && ok(rows_to, k)) pool[(long long)rows_to[k] * p.row_vec + col] = x[i];
             }
         };
         read(v[0], 0);
@@ -248,6 +260,8 @@ __global__ void __launch_bounds__(kCopyThreads)
         return;
     }
     if (s == d) return;
+    // checked build: both are pages of the pool
+    if (!in_range(i < n && s < num_blocks && d < num_blocks, status, nullptr)) return;
     const long long at = (long long)chunk * kCopyThreads * kCopyUnroll + threadIdx.x;
     uint4 k[kCopyUnroll], v[kCopyUnroll];
 #pragma unroll
@@ -286,6 +300,8 @@ __global__ void __launch_bounds__(kTableThreads)
     }
     const int k = chunk * kTableThreads + threadIdx.x;
     if (k < first[n] || k >= last[n] || k >= max_blocks) return;
+    // checked build: the entry is one of the table's
+    if (!in_range(k >= 0 && row < R, status, nullptr)) return;
     // taken out of the table at once, so that an entry named twice is given back once
     const int page = atomicExch(&tables[(long long)row * max_blocks + k], -1);
     if (page < 0) return;
@@ -293,6 +309,7 @@ __global__ void __launch_bounds__(kTableThreads)
         record_status(status, ATTN_ERR_DEVICE_BOUNDS);
         return;
     }
+    if (!in_range(page >= 0 && page < num_blocks, status, nullptr)) return;
     if (atomicSub(&refs[page], 1) <= 0) {  // not held: put the count back
         atomicAdd(&refs[page], 1);
         record_status(status, ATTN_ERR_DEVICE_BOUNDS);
@@ -341,6 +358,11 @@ __global__ void __launch_bounds__(kTableThreads) fork_kernel(const ForkParams p)
     const int len = fork_len(p, par, report);
     const int full = len >> p.shift;
     const bool part = len & ((1 << p.shift) - 1);
+    // checked build: both rows are the table's, and the part-filled page's entry is the row's
+    if (!in_range(n < p.N && par >= 0 && par < p.R && chi >= 0 && chi < p.R && full <= p.max_blocks &&
+                      (!part || full < p.max_blocks),
+                  p.status, nullptr))
+        return;
     const int32_t *from = p.tables + (long long)par * p.max_blocks;
     int32_t *to = p.tables + (long long)chi * p.max_blocks;
     const int k = chunk * kTableThreads + threadIdx.x;
@@ -350,7 +372,7 @@ __global__ void __launch_bounds__(kTableThreads) fork_kernel(const ForkParams p)
             record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
             page = -1;
         }
-        if (page >= 0) atomicAdd(&p.refs[page], 1);
+        if (page >= 0 && in_range(page < p.num_blocks, p.status, nullptr)) atomicAdd(&p.refs[page], 1);
         to[k] = page;
     }
     if (report) {
@@ -404,7 +426,9 @@ __device__ __forceinline__ int block_exclusive(int v, int *warp_sums, int &total
 
 // The first `need` free pages, in increasing order, into `list`; returns how many there
 // are (at most `need`).  Whole block.
-__device__ int free_pages(const int32_t *refs, int num_blocks, int need, int32_t *list, int *warp_sums) {
+// checked build: `room` is the length of `list`.
+__device__ int free_pages(const int32_t *refs, int num_blocks, int need, int32_t *list, long long room,
+                          int *warp_sums, int *status) {
     constexpr int kPer = 16;
     int found = 0;
     for (long long at = 0; at < num_blocks && found < need; at += kAllocThreads * kPer) {
@@ -423,7 +447,7 @@ __device__ int free_pages(const int32_t *refs, int num_blocks, int need, int32_t
         }
         int total;
         int rank = found + block_exclusive(__popc(free_mask), warp_sums, total);
-        while (free_mask && rank < need) {
+        while (free_mask && rank < need && in_range(rank < room, status, nullptr)) {
             list[rank++] = static_cast<int32_t>(first) + __ffs(free_mask) - 1;
             free_mask &= free_mask - 1;
         }
@@ -444,7 +468,7 @@ __global__ void __launch_bounds__(kAllocThreads) fork_alloc_kernel(const ForkPar
         block_exclusive(n < p.N && p.copy_src[n] >= 0, warp_sums, total);
         need += total;
     }
-    const int got = free_pages(p.refs, p.num_blocks, need, list, warp_sums);
+    const int got = free_pages(p.refs, p.num_blocks, need, list, p.N, warp_sums, p.status);
     if (got < need && threadIdx.x == 0) record_no_pages(p.status);
     int before = 0;
     for (int n0 = 0; n0 < p.N; n0 += kAllocThreads) {
@@ -458,6 +482,11 @@ __global__ void __launch_bounds__(kAllocThreads) fork_alloc_kernel(const ForkPar
             if (mine && rank < got) {
                 page = list[rank];
                 const int full = fork_len(p, p.parents[n], false) >> p.shift;
+                // checked build: a page of the pool, an entry of the table
+                if (!in_range(rank < p.N && page >= 0 && page < p.num_blocks && full < p.max_blocks &&
+                                  p.children[n] >= 0 && p.children[n] < p.R,
+                              p.status, nullptr))
+                    continue;
                 p.tables[(long long)p.children[n] * p.max_blocks + full] = page;
                 p.refs[page] = 1;
             }
@@ -475,6 +504,7 @@ struct ExtendParams {
     int32_t *offsets, *list;  // workspace: R + 1 and min(R * max_blocks, num_blocks)
     int R, max_blocks, num_blocks, shift;
     int *status;
+    __device__ long long room() const { return min((long long)R * max_blocks, (long long)num_blocks); }
 };
 
 __device__ __forceinline__ void extend_range(const ExtendParams &p, int r, bool report, int &k0, int &k1) {
@@ -496,6 +526,8 @@ __global__ void __launch_bounds__(kAllocThreads) extend_kernel(const ExtendParam
     for (int r = warp; r < p.R; r += kAllocThreads / 32) {
         int k0, k1, n = 0;
         extend_range(p, r, lane == 0, k0, k1);
+        // checked build: the entries are the row's
+        if (!in_range(k0 >= 0 && k1 <= p.max_blocks, p.status, nullptr)) k1 = k0;
         for (int k = k0 + lane; k < k1; k += 32) n += p.tables[(long long)r * p.max_blocks + k] < 0;
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) p.offsets[r] = n;
@@ -511,11 +543,12 @@ __global__ void __launch_bounds__(kAllocThreads) extend_kernel(const ExtendParam
     }
     const int need = static_cast<int>(min(need_all, (long long)p.num_blocks));
     if (need == 0) return;
-    const int got = free_pages(p.refs, p.num_blocks, need, p.list, warp_sums);
+    const int got = free_pages(p.refs, p.num_blocks, need, p.list, p.room(), warp_sums, p.status);
     if (got < need_all && threadIdx.x == 0) record_no_pages(p.status);
     for (int r = warp; r < p.R; r += kAllocThreads / 32) {
         int k0, k1;
         extend_range(p, r, false, k0, k1);
+        if (!in_range(k0 >= 0 && k1 <= p.max_blocks, p.status, nullptr)) k1 = k0;
         int rank = p.offsets[r];
         for (int kb = k0; kb < k1; kb += 32) {
             const int k = kb + lane;
@@ -523,10 +556,12 @@ __global__ void __launch_bounds__(kAllocThreads) extend_kernel(const ExtendParam
             const bool empty = k < k1 && *e < 0;
             const uint32_t vote = __ballot_sync(0xffffffffu, empty);
             const int mine = rank + __popc(vote & ((1u << lane) - 1u));
-            if (empty && mine < got) {
+            if (empty && mine < got && in_range(mine < p.room(), p.status, nullptr)) {
                 const int page = p.list[mine];
-                *e = page;
-                p.refs[page] = 1;
+                if (in_range(page >= 0 && page < p.num_blocks, p.status, nullptr)) {
+                    *e = page;
+                    p.refs[page] = 1;
+                }
             }
             rank += __popc(vote);
         }
@@ -550,6 +585,7 @@ attn_status_t launch_cache_append(const CacheArgs &a, cudaStream_t stream) {
     p.tables = a.block_tables;
     p.start = a.start;
     p.n_new = a.counts;
+    p.B = a.B;
     p.Hkv = a.Hkv;
     p.T = a.T;
     p.vec = a.D / 8;

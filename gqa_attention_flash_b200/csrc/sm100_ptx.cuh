@@ -20,8 +20,10 @@ __device__ __forceinline__ void record_status(int *status, int code) {
 }
 
 // Checked build (compiled with GQA_ATTN_DEBUG, library libgqa_attn_debug.so):
-// every TMA coordinate and every global index a kernel is about to use is
-// range-checked first.  A failed check records ATTN_ERR_DEVICE_BOUNDS, raises the
+// every TMA coordinate, and every global index that a kernel derives from data, from
+// a list of work or from a split (workspace slots, table entries, pool rows, pages,
+// output rows of such an item), is range-checked before it is used.  Indices that are
+// the grid's and the call's sizes alone are not.  A failed check records ATTN_ERR_DEVICE_BOUNDS, raises the
 // block's abort flag (so every role heads for its exit path, as after a bounded
 // wait that ran out) and the access is skipped; nothing traps.  In the normal
 // build in_range() is the constant true and the checks compile to nothing.
