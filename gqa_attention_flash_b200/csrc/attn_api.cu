@@ -425,11 +425,28 @@ namespace {
 // add tile and slice offsets to positions in 32 bits.
 constexpr long long kMaxPositions = 1ll << 30;
 
-// attn_decode (window = 0) and attn_decode_sinks.
+// Slices per (sequence, KV head) when the caller leaves them to the library: enough for
+// two blocks per SM, and at most one per 64-key tile that can hold a visible key.  Up to 8
+// slices need no workspace and no second kernel, so more are made only where 8 would be
+// left with more than 32 tiles each.  0: the device cannot be asked for its SMs.
+int sink_splits(int B, int Hkv, long long S_cap, int window, int sinks) {
+    int dev = 0, n_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n_sm < 1)
+        return 0;
+    const long long tiles = std::min((std::min<long long>(window, S_cap) + 62) / 64 + 1 +
+                                         (std::min<long long>(sinks, S_cap) + 63) / 64,
+                                     (S_cap + 63) / 64);
+    const long long pairs = std::max(1ll, (long long)B * Hkv);
+    const long long n = std::max(1ll, std::min({(2ll * n_sm + pairs - 1) / pairs, tiles, 64ll}));
+    return static_cast<int>(n > 8 && tiles <= 8 * 32 ? 8 : n);
+}
+
+// attn_decode (window = 0) and attn_decode_sinks (where n_splits may be 0).
 attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const void *V,
                                 const int32_t *lengths, int window, int sinks, int n_splits,
                                 void *stream, int B, int Hq, int Hkv, int S_cap, int D) {
-    if (B < 0 || Hq < 1 || Hkv < 1 || S_cap < 0 || n_splits < 1 || n_splits > 64)
+    if (B < 0 || Hq < 1 || Hkv < 1 || S_cap < 0 || n_splits < (window > 0 ? 0 : 1) || n_splits > 64)
         return ATTN_ERR_INVALID;
     if (Hq % Hkv != 0 || Hq / Hkv > 16 || Hkv > 65535) return ATTN_ERR_INVALID;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
@@ -441,6 +458,8 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
         return ATTN_ERR_INVALID;
     if ((long long)B * Hkv > 0x7fffffffll) return ATTN_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n_splits == 0 && (n_splits = sink_splits(B, Hkv, S_cap, window, sinks)) == 0)
+        return answer(ATTN_ERR_CUDA);
     const size_t bytes = decode_workspace_floats(B, Hq, n_splits, D) * sizeof(float);
     const bool needs_ws = window == 0 || !decode_sinks_in_cluster(n_splits);
     void *ws = nullptr;
@@ -465,19 +484,6 @@ attn_status_t decode_contiguous(void *O, const void *Q, const void *K, const voi
     return answer(st);
 }
 
-// Slices per (sequence, KV head) when the caller leaves them to the library: enough for
-// two blocks per SM, and at most one per 64-key tile that can hold a visible key.  Up to 8
-// slices need no workspace and no second kernel, so more are made only where 8 would be
-// left with more than 32 tiles each.
-int sink_splits(int B, int Hkv, long long S_cap, int window, int sinks) {
-    const long long tiles = std::min((std::min<long long>(window, S_cap) + 62) / 64 + 1 +
-                                         (std::min<long long>(sinks, S_cap) + 63) / 64,
-                                     (S_cap + 63) / 64);
-    const long long pairs = std::max(1ll, (long long)B * Hkv);
-    const long long n = std::max(1ll, std::min({(2 * 148 + pairs - 1) / pairs, tiles, 64ll}));
-    return static_cast<int>(n > 8 && tiles <= 8 * 32 ? 8 : n);
-}
-
 }  // namespace
 
 attn_status_t attn_decode(void *O, const void *Q, const void *K, const void *V,
@@ -492,8 +498,6 @@ attn_status_t attn_decode_sinks(void *O, const void *Q, const void *K, const voi
                                 void *stream, int B, int Hq, int Hkv, int S_cap, int D) {
     NvtxRange nvtx_range("attn_decode_sinks");
     if (window < 1 || sinks < 0 || S_cap > kMaxPositions) return ATTN_ERR_INVALID;
-    if (n_splits == 0 && B >= 0 && Hkv >= 1 && S_cap >= 0)
-        n_splits = sink_splits(B, Hkv, S_cap, window, sinks);
     return decode_contiguous(O, Q, K, V, lengths, window, sinks, n_splits, stream, B, Hq, Hkv, S_cap,
                              D);
 }
@@ -626,13 +630,13 @@ attn_status_t attn_rbs_block_mask(uint8_t *block_mask, float *base_scores, float
 
 namespace {
 
-// attn_decode_paged (window = 0) and attn_decode_paged_sinks.
+// attn_decode_paged (window = 0) and attn_decode_paged_sinks (where n_splits may be 0).
 attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const void *V_cache,
                            const int32_t *block_tables, const int32_t *seq_lens, int window,
                            int sinks, int n_splits, void *stream, int B, int Hq, int Hkv,
                            int num_blocks, int block_size, int max_blocks_per_seq, int D) {
-    if (B < 0 || Hq < 1 || Hkv < 1 || num_blocks < 1 || max_blocks_per_seq < 0 || n_splits < 1 ||
-        n_splits > 64)
+    if (B < 0 || Hq < 1 || Hkv < 1 || num_blocks < 1 || max_blocks_per_seq < 0 ||
+        n_splits < (window > 0 ? 0 : 1) || n_splits > 64)
         return ATTN_ERR_INVALID;
     if (block_size < 8 || block_size > 65536 || (block_size & (block_size - 1)) != 0)
         return ATTN_ERR_INVALID;
@@ -648,6 +652,9 @@ attn_status_t decode_paged(void *O, const void *Q, const void *K_cache, const vo
         ((reinterpret_cast<uintptr_t>(seq_lens) | reinterpret_cast<uintptr_t>(block_tables)) & 3u))
         return ATTN_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n_splits == 0 &&
+        (n_splits = sink_splits(B, Hkv, (long long)max_blocks_per_seq * block_size, window, sinks)) == 0)
+        return answer(ATTN_ERR_CUDA);
     const size_t bytes = decode_workspace_floats(B, Hq, n_splits, D) * sizeof(float);
     const bool needs_ws = window == 0 || !decode_sinks_in_cluster(n_splits);
     void *ws = nullptr;
@@ -709,8 +716,6 @@ attn_status_t attn_decode_paged_sinks(void *O, const void *Q, const void *K_cach
     NvtxRange nvtx_range("attn_decode_paged_sinks");
     if (window < 1 || sinks < 0) return ATTN_ERR_INVALID;
     if ((long long)max_blocks_per_seq * block_size > kMaxPositions) return ATTN_ERR_INVALID;
-    if (n_splits == 0 && B >= 0 && Hkv >= 1 && max_blocks_per_seq >= 0 && block_size > 0)
-        n_splits = sink_splits(B, Hkv, (long long)max_blocks_per_seq * block_size, window, sinks);
     return decode_paged(O, Q, K_cache, V_cache, block_tables, seq_lens, window, sinks, n_splits, stream,
                         B, Hq, Hkv, num_blocks, block_size, max_blocks_per_seq, D);
 }

@@ -12,7 +12,7 @@ struct Entry {
     const void *stream, *what;
 };
 std::vector<Entry> g_log;
-int g_calls = 0, g_fail_at = -1;
+int g_calls = 0, g_fail_at = -1, g_sms = 148, g_grid_x = 0;
 long long g_next = 0;
 
 cudaError_t g_last = cudaSuccess;  // what cudaGetLastError answers
@@ -43,6 +43,8 @@ void fake_reset(int fail_at) {
 }
 void fake_set_last_error(int e) { g_last = static_cast<cudaError_t>(e); }
 int fake_last_error() { return static_cast<int>(g_last); }
+void fake_set_sms(int n) { g_sms = n; }
+int fake_last_grid_x() { return g_grid_x; }
 int fake_calls() { return g_calls; }
 int fake_log_size() { return static_cast<int>(g_log.size()); }
 void fake_log(int i, int *kind, const void **stream, const void **what) {
@@ -66,7 +68,7 @@ cudaError_t cudaGetDevice(int *d) {
     return fails() ? cudaErrorUnknown : cudaSuccess;
 }
 cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr, int) {
-    *v = 148;
+    *v = g_sms;
     return fails() ? cudaErrorUnknown : cudaSuccess;
 }
 cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int *n, const void *, int, size_t, unsigned) {
@@ -107,6 +109,7 @@ cudaError_t cudaFreeAsync(void *p, cudaStream_t s) {
 }
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const void *f, void **) {
     if (fails()) return cudaErrorUnknown;
+    g_grid_x = static_cast<int>(c->gridDim.x);
     note(kLaunch, c->stream, f);
     return cudaSuccess;
 }

@@ -93,6 +93,9 @@ CALLS = {
                                           STREAM),
     "decode": lambda L: L.attn_decode_sinks(P, P, P, P, P, 64, 4, 4, STREAM, 2, 8, 2, 512, 128),
     "decode, workspace": lambda L: L.attn_decode_sinks(P, P, P, P, P, 64, 4, 16, STREAM, 2, 8, 2, 512, 128),
+    "decode, slices chosen": lambda L: L.attn_decode_sinks(P, P, P, P, P, 64, 4, 0, STREAM, 2, 8, 2, 512, 128),
+    "paged decode, slices chosen": lambda L: L.attn_decode_paged_sinks(P, P, P, P, P, P, 64, 4, 0, STREAM, 2, 8, 2,
+                                                                       9, 16, 4, 128),
     "paged decode": lambda L: L.attn_decode_paged_sinks(P, P, P, P, P, P, 64, 4, 16, STREAM, 2, 8, 2, 9, 16, 4,
                                                         128),
     "tree": lambda L: L.attn_tree_paged(P, P, P, P, P, P, P, None, STREAM, 2, 8, 2, 5, 9, 16, 4, 128),
@@ -136,3 +139,16 @@ def test_an_error_of_other_code_is_not_the_calls(objects, name):
     lib.fake_set_last_error(2)
     assert CALLS[name](lib) == OK
     assert lib.fake_last_error() == 2
+
+
+def test_slices_of_the_windowed_decode_follow_the_devices_sms(objects):
+    lib = fresh(objects)
+    lib.fake_reset(-1)
+    # two (sequence, KV head) pairs, 512 key tiles: two blocks for each SM
+    for sms, slices in ((148, 64), (8, 8), (6, 6), (1, 1)):
+        lib.fake_set_sms(sms)
+        assert lib.attn_decode_sinks(P, P, P, P, P, 1 << 15, 4, 0, STREAM, 1, 8, 2, 1 << 15, 128) == OK
+        if slices > 8:  # the combine came last, 8 heads in blocks of 4
+            assert lib.fake_last_grid_x() == 2
+        else:
+            assert lib.fake_last_grid_x() == slices
