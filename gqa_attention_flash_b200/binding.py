@@ -99,7 +99,8 @@ def _ptr(t):
 def _i32(v, name):
     """An integer of the C ABI (ctypes would cut a wider one to its low 32 bits: 2**32 sinks
     to none)."""
-    v = int(v)
+    if type(v) is not int:
+        v = int(v)
     if not -0x80000000 <= v <= 0x7fffffff:
         raise ValueError(f"{name} = {v} does not fit in 32 bits")
     return v

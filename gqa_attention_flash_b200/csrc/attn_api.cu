@@ -694,7 +694,8 @@ attn_status_t validate_pool(int num_blocks, int block_size, int max_blocks) {
     return ATTN_OK;
 }
 
-// int32 arrays of the cache operators: given, and 16-byte aligned where read in vectors.
+// Alignment of int32 arrays (ref_counts, which fork and extend read in 16-byte vectors, is
+// checked with aligned16 there).
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace

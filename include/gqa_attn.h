@@ -397,7 +397,8 @@ attn_status_t attn_tree_paged(void *O, const void *Q, const void *K_cache, const
  * free on the table.
  *   ref_counts int32 (num_blocks): how many table entries name each page.  A page is
  *   free when its count is 0; fork and extend hand out the lowest free pages first, so
- *   their results depend on their arguments alone.
+ *   their results depend on their arguments alone.  Like every tensor, ref_counts is
+ *   16-byte aligned; the other int32 arrays need 4 bytes.
  * block_size is a power of two >= 8, max_blocks_per_seq >= 1, num_blocks >= 1, and
  * num_blocks * block_size and max_blocks_per_seq * block_size below 2^31.  Calls that
  * share a table, counts or pages are to be ordered by the caller (one stream).
